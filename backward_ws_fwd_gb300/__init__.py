@@ -1,12 +1,15 @@
 """backward_ws_fwd_gb300 — Python binding of libwsfwd (C ABI in include/wsf.h).
 
-Forward and backward (vector-Jacobian product) kernels of two memory-bound
-row operators on one GB300 GPU:
+Forward and backward (vector-Jacobian product) kernels of memory-bound row
+operators on one GB300 GPU:
 
 * weighted sum  y[i] = Σ_d x[i,d]·w[d]   ("Writing Triton Kernels with
   Autograd: A Minimal End-to-End Example", §1–§5)
 * scaled SiLU   y = w·x·sigmoid(x)        ("Backward in Triton —
   autograd.Function and the backward grid", § A complete minimal example)
+* row softmax, RMSNorm and LayerNorm
+* rotary positions, the top-k router with its balance loss, and group norm
+  with an activation (block.py)
 
 This module only marshals torch tensors into the C entry points: pointers,
 sizes, the storage-type code and the current CUDA stream.  Every step runs
@@ -410,9 +413,15 @@ def selftest_waiting_warps() -> int:
     return int(lib.wsf_selftest_waiting_warps())
 
 
+from .block import (ACT_NONE, ACT_SILU, groupnorm_bwd, groupnorm_fwd,  # noqa: E402
+                    groupnorm_workspace_bytes, rotary_bwd, rotary_frequencies, rotary_fwd,
+                    router_bwd, router_fwd, router_fwd_workspace_bytes)
+
 __all__ = ["lib", "LIB_PATH", "WsfError", "status_string", "cluster_wait_timeouts",
            "selftest_exchange_timeout", "selftest_waiting_warps", "ws_fwd", "ws_bwd", "ws_bwd_noalloc",
            "ws_bwd_atomic", "silu_bwd_atomic", "softmax_fwd", "softmax_bwd", "silu_fwd",
            "silu_bwd", "rmsnorm_fwd", "rmsnorm_bwd", "layernorm_fwd", "layernorm_bwd",
            "ws_bwd_workspace_bytes", "silu_bwd_workspace_bytes", "norm_bwd_workspace_bytes", "F32",
-           "F16", "BF16"]
+           "F16", "BF16", "rotary_fwd", "rotary_bwd", "rotary_frequencies", "router_fwd",
+           "router_bwd", "router_fwd_workspace_bytes", "groupnorm_fwd", "groupnorm_bwd",
+           "groupnorm_workspace_bytes", "ACT_NONE", "ACT_SILU"]

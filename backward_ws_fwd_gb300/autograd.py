@@ -12,7 +12,9 @@ RMSNorm and LayerNorm follow "Backward in Triton — autograd.Function and
 the backward grid", § Save vs recompute: the forward saves only x and the
 parameters, and the backward recomputes the row statistics from x.  Softmax
 saves its output y, from which its backward is formed ("Backprop for kernel
-writers", §04 The duality: dx = y ⊙ (dy − Σ dy·y)).
+writers", §04 The duality: dx = y ⊙ (dy − Σ dy·y)).  Rotary positions save
+no activations (the map is linear), the router its logits, choice and counts,
+group norm x and its statistics.
 
 Gradient accumulation across micro-batches ("fp32 accumulation, and why
 gradients use +=") happens in PyTorch's engine, which adds each returned
@@ -24,7 +26,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (layernorm_bwd, layernorm_fwd, rmsnorm_bwd, rmsnorm_fwd, silu_bwd, silu_fwd,
+from . import (groupnorm_bwd, groupnorm_fwd, layernorm_bwd, layernorm_fwd, rmsnorm_bwd,
+               rmsnorm_fwd, rotary_bwd, rotary_fwd, router_bwd, router_fwd, silu_bwd, silu_fwd,
                softmax_bwd, softmax_fwd, ws_bwd, ws_fwd)
 
 _STORAGE = (torch.float32, torch.float16, torch.bfloat16)
@@ -157,6 +160,105 @@ class SoftmaxFunction(torch.autograd.Function):
         return softmax_bwd(y, dy).reshape(ctx.x_shape)
 
 
+def _heads(x: torch.Tensor) -> torch.Tensor:
+    """x with unit inner stride (other strides are kept)."""
+    return x if x.shape[-1] <= 1 or x.stride(-1) == 1 else x.contiguous()
+
+
+class RotaryFunction(torch.autograd.Function):
+    """Rotary positions of q and k (k may be None); see rotary_fwd.  Positions
+    and frequencies are constants."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, scale=1.0, interleaved=False):
+        if q.dtype not in _STORAGE:
+            raise TypeError("q must be float32/float16/bfloat16")
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.scale, ctx.interleaved, ctx.has_k = scale, interleaved, k is not None
+        yq, yk = rotary_fwd(_heads(q), None if k is None else _heads(k), positions, inv_freq,
+                            scale, interleaved)
+        return yq, yk
+
+    @staticmethod
+    def backward(ctx, dyq, dyk):
+        positions, inv_freq = ctx.saved_tensors
+        turn = (positions, inv_freq, ctx.scale, ctx.interleaved)
+        need_q, need_k = ctx.needs_input_grad[:2]
+        need_k = need_k and ctx.has_k
+        dq = dk = None
+        if need_q and need_k:
+            dq, dk = rotary_bwd(_heads(dyq), _heads(dyk), *turn)
+        elif need_q:
+            dq, _ = rotary_bwd(_heads(dyq), None, *turn)
+        elif need_k:
+            dk, _ = rotary_bwd(_heads(dyk), None, *turn)
+        return dq, dk, None, None, None, None
+
+
+class RouterFunction(torch.autograd.Function):
+    """Top-k routing: (gates, ids, counts, loss) of router_fwd for logits of
+    any leading shape; ids and counts are not differentiable."""
+
+    @staticmethod
+    def forward(ctx, logits, k, mask=None, renormalize=False):
+        if logits.dtype not in _STORAGE:
+            raise TypeError("logits must be float32/float16/bfloat16")
+        lead = logits.shape[:-1]
+        l2 = _rows(logits)
+        if mask is not None:
+            mask = mask.reshape(-1).contiguous()
+        gates, ids, counts, loss = router_fwd(l2, k, mask, renormalize)
+        ctx.save_for_backward(l2, ids, counts)
+        ctx.renormalize, ctx.shape = renormalize, logits.shape
+        gates, shown = gates.reshape(*lead, k), ids.reshape(*lead, k)
+        ctx.mark_non_differentiable(shown, counts)
+        return gates, shown, counts, loss
+
+    @staticmethod
+    def backward(ctx, dgates, _ids, _counts, dloss):
+        l2, ids, counts = ctx.saved_tensors
+        dgates = dgates.reshape(ids.shape).contiguous()
+        dl = router_bwd(l2, ids, counts, dgates, dloss.contiguous(), ctx.renormalize)
+        return dl.reshape(ctx.shape), None, None, None
+
+
+class GroupNormFunction(torch.autograd.Function):
+    """Group norm over channels-last x [N, ..., C] with an optional SiLU; w, b
+    float32 [C]; see groupnorm_fwd."""
+
+    @staticmethod
+    def forward(ctx, x, w, b, groups, eps=1e-5, act=None):
+        if x.dtype not in _STORAGE or w.dtype != torch.float32 or b.dtype != torch.float32:
+            raise TypeError("x must be float32/float16/bfloat16, w and b float32")
+        x3 = GroupNormFunction._nsc(x)
+        w, b = w.contiguous(), b.contiguous()
+        y, mean, rstd = groupnorm_fwd(x3, w, b, groups, eps, act)
+        ctx.save_for_backward(x3, w, b, mean, rstd)
+        ctx.groups, ctx.act, ctx.x_shape = groups, act, x.shape
+        return y.reshape(x.shape)
+
+    @staticmethod
+    def _nsc(x):
+        if x.dim() < 2:
+            raise ValueError("x must be [N, ..., C]")
+        S = 1
+        for n in x.shape[1:-1]:
+            S *= n
+        x3 = x.reshape(x.shape[0], S, x.shape[-1])
+        if x3.shape[2] > 1 and x3.stride(2) != 1 or (S > 1 and x3.stride(1) < x3.shape[2]):
+            x3 = x3.contiguous()
+        return x3
+
+    @staticmethod
+    def backward(ctx, dy):
+        x3, w, b, mean, rstd = ctx.saved_tensors
+        dy = GroupNormFunction._nsc(dy.reshape(ctx.x_shape))
+        dx, gw, gb = groupnorm_bwd(x3, w, b, mean, rstd, dy, ctx.groups, ctx.act)
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        return ((dx.reshape(ctx.x_shape) if need_x else None), (gw if need_w else None),
+                (gb if need_b else None), None, None, None)
+
+
 def softmax(x: torch.Tensor) -> torch.Tensor:
     return SoftmaxFunction.apply(x)
 
@@ -175,6 +277,21 @@ def weighted_sum(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
 
 def scaled_silu(x: torch.Tensor, w: torch.Tensor, inplace: bool = False) -> torch.Tensor:
     return ScaledSiLUFunction.apply(x, w, inplace)
+
+
+def rotary(q, k, positions, inv_freq, scale: float = 1.0, interleaved: bool = False):
+    """(q, k) [B, S, H, D] (or [T, H, D]) at their positions; k may be None."""
+    return RotaryFunction.apply(q, k, positions, inv_freq, scale, interleaved)
+
+
+def topk_router(logits, k: int, mask=None, renormalize: bool = False):
+    """(gates, ids, counts, balance loss) of logits [..., E]."""
+    return RouterFunction.apply(logits, k, mask, renormalize)
+
+
+def group_norm(x, w, b, groups: int, eps: float = 1e-5, act=None):
+    """Group norm of channels-last x [N, ..., C], act None or "silu"."""
+    return GroupNormFunction.apply(x, w, b, groups, eps, act)
 
 
 class WeightedSum(torch.nn.Module):
@@ -224,3 +341,17 @@ class LayerNorm(torch.nn.Module):
 
     def forward(self, x):
         return layer_norm(x, self.weight, self.bias, self.eps)
+
+
+class GroupNorm(torch.nn.Module):
+    """Group norm over channels-last values [N, ..., C] with learnable fp32
+    scale and shift and an optional activation (act="silu")."""
+
+    def __init__(self, groups: int, C: int, eps: float = 1e-5, act=None, device=None):
+        super().__init__()
+        self.groups, self.eps, self.act = groups, eps, act
+        self.weight = torch.nn.Parameter(torch.ones(C, dtype=torch.float32, device=device))
+        self.bias = torch.nn.Parameter(torch.zeros(C, dtype=torch.float32, device=device))
+
+    def forward(self, x):
+        return group_norm(x, self.weight, self.bias, self.groups, self.eps, self.act)

@@ -1,0 +1,375 @@
+// abi_block.cu — the extern "C" entry points of the block operators (rotary,
+// router, group norm) declared in include/wsf.h.  As in abi.cu, every
+// argument is validated on the host before anything is enqueued.
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "wsf.h"
+#include "wsf_block.h"
+#include "wsf_internal.h"
+
+namespace {
+
+using wsf::elt_bytes;
+
+bool valid_dtype(int dtype) { return dtype == WSF_F32 || dtype == WSF_F16 || dtype == WSF_BF16; }
+
+bool aligned_to(const void* p, int a) { return (uintptr_t)p % (uintptr_t)a == 0; }
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? WSF_OK : WSF_ERR_CUDA; }
+
+// acc += (extent - 1)·stride, false on overflow of int64 (all non-negative)
+bool reach(int64_t extent, int64_t stride, int64_t* acc) {
+    int64_t m;
+    return !__builtin_mul_overflow(extent - 1, stride, &m) && !__builtin_add_overflow(*acc, m, acc);
+}
+
+struct Span {
+    uintptr_t lo, hi;  // [lo, hi)
+};
+
+Span span(const void* p, int64_t bytes) {
+    return Span{(uintptr_t)p, (uintptr_t)p + (uintptr_t)(bytes > 0 ? bytes : 0)};
+}
+
+bool overlap(Span a, Span b) {
+    if (a.lo == a.hi || b.lo == b.hi) return false;
+    return a.lo < b.hi && b.lo < a.hi;
+}
+
+// A strided [e0, e1, e2, inner] tensor with unit inner stride.
+struct Tensor {
+    const void* p;
+    int64_t e[3], st[3], inner;
+    int es;
+
+    bool empty() const { return !e[0] || !e[1] || !e[2] || !inner; }
+    // elements from the first to one past the last; -1 on overflow
+    int64_t extent() const {
+        if (empty()) return 0;
+        int64_t a = inner;
+        for (int i = 0; i < 3; i++)
+            if (!reach(e[i], st[i], &a)) return -1;
+        return a > INT64_MAX / 8 ? -1 : a;
+    }
+    Span bytes() const { return span(p, extent() * es); }
+    bool negative() const {
+        for (int i = 0; i < 3; i++)
+            if (e[i] > 1 && st[i] < 0) return true;
+        return false;
+    }
+    // no two elements share an address: ordered by stride, each dimension
+    // steps over everything inside it
+    bool distinct() const {
+        int o[3] = {0, 1, 2};
+        for (int i = 0; i < 2; i++)
+            for (int j = 0; j < 2 - i; j++)
+                if (st[o[j]] > st[o[j + 1]]) {
+                    const int t = o[j];
+                    o[j] = o[j + 1];
+                    o[j + 1] = t;
+                }
+        int64_t a = inner;
+        for (int i = 0; i < 3; i++) {
+            const int k = o[i];
+            if (e[k] <= 1) continue;
+            if (st[k] < a) return false;
+            a += (e[k] - 1) * st[k];
+        }
+        return true;
+    }
+    bool same(const Tensor& t) const {
+        if (p != t.p) return false;
+        for (int i = 0; i < 3; i++)
+            if (e[i] != t.e[i] || (e[i] > 1 && st[i] != t.st[i])) return false;
+        return true;
+    }
+};
+
+// Whether two tensors share no byte.  Views that interleave in one buffer are
+// told apart where they repeat with the same period (the batch or the token
+// stride): what each covers of a period has to be apart.
+bool apart(const Tensor& a, const Tensor& b) {
+    if (!overlap(a.bytes(), b.bytes())) return true;
+    for (int d = 0; d < 2; d++) {
+        const int64_t period = a.st[d];
+        if (a.e[d] <= 1 || b.e[d] <= 1 || period <= 0 || b.st[d] != period) continue;
+        int64_t ia = a.inner, ib = b.inner;
+        bool ok = true;
+        for (int i = 0; i < 3; i++) {
+            if (i == d) continue;
+            if (i < d) {  // an outer dimension keeps the pattern if it steps whole periods
+                ok = ok && (a.e[i] <= 1 || a.st[i] % period == 0) &&
+                     (b.e[i] <= 1 || b.st[i] % period == 0);
+                continue;
+            }
+            ia += (a.e[i] - 1) * a.st[i];
+            ib += (b.e[i] - 1) * b.st[i];
+        }
+        if (!ok || ia > period || ib > period) continue;
+        const int64_t pb = period * a.es;
+        int64_t gap = (int64_t)((uintptr_t)b.p - (uintptr_t)a.p) % pb;
+        if (gap < 0) gap += pb;
+        if (gap >= ia * a.es && gap + ib * b.es <= pb) return true;
+    }
+    return false;
+}
+
+int rotary_entry(const void* q, const int64_t* qs, void* yq, const int64_t* yqs, int64_t Hq,
+                 const void* k, const int64_t* ks, void* yk, const int64_t* yks, int64_t Hk,
+                 const void* pos, int64_t ld_pos, int pos_bytes, const float* inv_freq, float scale,
+                 int layout, float sign, int64_t B, int64_t S, int64_t D, int64_t R, int dtype,
+                 wsf_stream_t stream) {
+    if (!valid_dtype(dtype)) return WSF_ERR_BAD_DTYPE;
+    if (B < 0 || S < 0 || D < 0 || Hq < 0 || Hk < 0 || R < 0 || R > D || R > wsf::kRotaryMaxR ||
+        R % 2)
+        return WSF_ERR_BAD_SHAPE;
+    if ((layout != WSF_ROTARY_HALF && layout != WSF_ROTARY_INTERLEAVED) ||
+        (pos_bytes != 4 && pos_bytes != 8) || !isfinite(scale))
+        return WSF_ERR_BAD_ARG;
+    if (B == 0 || S == 0 || D == 0 || (Hq == 0 && Hk == 0)) return WSF_OK;
+    if (B > INT32_MAX / S || Hq > wsf::kRotaryMaxToken || Hk > wsf::kRotaryMaxToken ||
+        D > wsf::kRotaryMaxToken / (Hq + Hk))
+        return WSF_ERR_BAD_SHAPE;
+    if ((Hq && (!q || !yq || !qs || !yqs)) || (Hk && (!k || !yk || !ks || !yks)) ||
+        (R && (!pos || !inv_freq)))
+        return WSF_ERR_NULL_PTR;
+    const int es = elt_bytes(dtype);
+    static const int64_t none[3] = {0, 0, 0};
+    auto heads = [&](const void* p, const int64_t* st, int64_t H) {
+        if (!H) st = none;
+        return Tensor{p, {B, S, H}, {st[0], st[1], st[2]}, D, es};
+    };
+    const Tensor in[2] = {heads(q, qs, Hq), heads(k, ks, Hk)};
+    const Tensor out[2] = {heads(yq, yqs, Hq), heads(yk, yks, Hk)};
+    for (int i = 0; i < 2; i++) {
+        if (in[i].empty()) continue;
+        if (in[i].negative() || out[i].negative()) return WSF_ERR_BAD_STRIDE;
+        if (in[i].extent() < 0 || out[i].extent() < 0) return WSF_ERR_BAD_SHAPE;
+        if (!out[i].distinct()) return WSF_ERR_BAD_STRIDE;
+        if (!aligned_to(in[i].p, es) || !aligned_to(out[i].p, es)) return WSF_ERR_MISALIGNED;
+    }
+    if (B > 1 && (ld_pos < 0 || (ld_pos > 0 && ld_pos < S))) return WSF_ERR_BAD_STRIDE;
+    int64_t pe = S;
+    if (!reach(B, B > 1 ? ld_pos : 0, &pe) || pe > INT64_MAX / 8) return WSF_ERR_BAD_SHAPE;
+    if (R && (!aligned_to(pos, pos_bytes) || !aligned_to(inv_freq, 4))) return WSF_ERR_MISALIGNED;
+    const Span sp = span(pos, R ? pe * pos_bytes : 0), sf = span(inv_freq, R / 2 * 4);
+    for (int i = 0; i < 2; i++) {
+        if (out[i].empty()) continue;
+        const Span so = out[i].bytes();
+        if (overlap(so, sp) || overlap(so, sf)) return WSF_ERR_OVERLAP;
+        for (int j = 0; j < 2; j++) {
+            if (in[j].empty()) continue;
+            if (!(i == j && out[i].same(in[j])) && !apart(out[i], in[j])) return WSF_ERR_OVERLAP;
+        }
+    }
+    if (!out[0].empty() && !out[1].empty() && !apart(out[0], out[1])) return WSF_ERR_OVERLAP;
+    const wsf::RotaryHeads a{q, yq, in[0].st[0], in[0].st[1], in[0].st[2],
+                             out[0].st[0], out[0].st[1], out[0].st[2], Hq};
+    const wsf::RotaryHeads b{k, yk, in[1].st[0], in[1].st[1], in[1].st[2],
+                             out[1].st[0], out[1].st[1], out[1].st[2], Hk};
+    return cuda_status(wsf::launch_rotary(a, b, pos, B > 1 ? ld_pos : 0, pos_bytes, inv_freq,
+                                          scale, layout, sign, B, S, D, R, dtype,
+                                          (cudaStream_t)stream));
+}
+
+// The router's sizes and logits; *lb receives the span of [T, E] at stride ld.
+int router_sizes(int64_t T, int64_t E, int64_t k, int64_t ld, int es, int64_t* lb) {
+    if (T < 0 || E < 1 || E > wsf::kRouterMaxE || k < 1 || k > E || k > wsf::kRouterMaxK ||
+        T > INT32_MAX / k)
+        return WSF_ERR_BAD_SHAPE;
+    *lb = 0;
+    if (T == 0) return WSF_OK;
+    if (ld < E) return WSF_ERR_BAD_STRIDE;
+    int64_t a = E;
+    if (!reach(T, ld, &a) || a > INT64_MAX / 8) return WSF_ERR_BAD_SHAPE;
+    *lb = a * es;
+    return WSF_OK;
+}
+
+// First overlap of an output with an input or with an output before it.
+bool clash(const Span* outs, int no, const Span* ins, int ni) {
+    for (int i = 0; i < no; i++) {
+        for (int j = 0; j < ni; j++)
+            if (overlap(outs[i], ins[j])) return true;
+        for (int j = 0; j < i; j++)
+            if (overlap(outs[i], outs[j])) return true;
+    }
+    return false;
+}
+
+bool groupnorm_sizes(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
+    if (N < 0 || S < 0 || C < 0 || G < 1 || C > wsf::kGroupNormMaxC || C % G) return false;
+    // grids and workspaces stay inside int32 launches and int64 bytes
+    if (C == 0 || N == 0 || S == 0) return N <= INT32_MAX;
+    if (N > INT32_MAX || S > (INT64_MAX / 64) / C / N) return false;
+    return wsf::groupnorm_units(N, S, C, G, dtype) <= INT32_MAX && N * G <= INT32_MAX;
+}
+
+Tensor rows_of(const void* p, int64_t n, int64_t s, int64_t N, int64_t S, int64_t C, int es) {
+    return Tensor{p, {1, N, S}, {0, n, s}, C, es};
+}
+
+}  // namespace
+
+extern "C" {
+
+int rotary_fwd(const void* q, const int64_t* q_strides, void* yq, const int64_t* yq_strides,
+               int64_t Hq, const void* k, const int64_t* k_strides, void* yk,
+               const int64_t* yk_strides, int64_t Hk, const void* positions, int64_t ld_positions,
+               int position_bytes, const float* inv_freq, float scale, int layout, int64_t B,
+               int64_t S, int64_t D, int64_t R, int dtype, wsf_stream_t stream) {
+    return rotary_entry(q, q_strides, yq, yq_strides, Hq, k, k_strides, yk, yk_strides, Hk,
+                        positions, ld_positions, position_bytes, inv_freq, scale, layout, 1.0f, B,
+                        S, D, R, dtype, stream);
+}
+
+int rotary_bwd(const void* dyq, const int64_t* dyq_strides, void* dq, const int64_t* dq_strides,
+               int64_t Hq, const void* dyk, const int64_t* dyk_strides, void* dk,
+               const int64_t* dk_strides, int64_t Hk, const void* positions, int64_t ld_positions,
+               int position_bytes, const float* inv_freq, float scale, int layout, int64_t B,
+               int64_t S, int64_t D, int64_t R, int dtype, wsf_stream_t stream) {
+    return rotary_entry(dyq, dyq_strides, dq, dq_strides, Hq, dyk, dyk_strides, dk, dk_strides, Hk,
+                        positions, ld_positions, position_bytes, inv_freq, scale, layout, -1.0f, B,
+                        S, D, R, dtype, stream);
+}
+
+size_t router_fwd_workspace_bytes(int64_t T, int64_t E) {
+    if (T < 0 || E < 1 || E > wsf::kRouterMaxE) return SIZE_MAX;
+    return (size_t)(wsf::router_tiles(T, E) * E * 8);
+}
+
+int router_fwd(const void* logits, int64_t ld, const unsigned char* mask, int64_t k,
+               int renormalize, float* gates, int* ids, int* counts, float* loss, void* workspace,
+               size_t workspace_bytes, int64_t T, int64_t E, int dtype, wsf_stream_t stream) {
+    if (!valid_dtype(dtype)) return WSF_ERR_BAD_DTYPE;
+    if (renormalize != 0 && renormalize != 1) return WSF_ERR_BAD_ARG;
+    const int es = elt_bytes(dtype);
+    int64_t lb;
+    const int rc = router_sizes(T, E, k, ld, es, &lb);
+    if (rc != WSF_OK) return rc;
+    if (!counts || !loss || (T && (!logits || !gates || !ids))) return WSF_ERR_NULL_PTR;
+    if (!aligned_to(logits, es) || !aligned_to(gates, 4) || !aligned_to(ids, 4) ||
+        !aligned_to(counts, 4) || !aligned_to(loss, 4) || !aligned_to(workspace, 4))
+        return WSF_ERR_MISALIGNED;
+    const size_t need = router_fwd_workspace_bytes(T, E);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WSF_ERR_WORKSPACE;
+    const Span ins[2] = {span(logits, lb), span(mask, mask ? T : 0)};
+    const Span outs[5] = {span(gates, T * k * 4), span(ids, T * k * 4), span(counts, E * 4),
+                          span(loss, 4), span(workspace, (int64_t)need)};
+    if (clash(outs, 5, ins, 2)) return WSF_ERR_OVERLAP;
+    return cuda_status(wsf::launch_router_fwd(logits, ld, mask, k, renormalize, gates, ids, counts,
+                                              loss, workspace, T, E, dtype,
+                                              (cudaStream_t)stream));
+}
+
+int router_bwd(const void* logits, int64_t ld, const int* ids, const int* counts, int64_t k,
+               int renormalize, const float* dgates, const float* dloss, void* dlogits,
+               int64_t ldd, int64_t T, int64_t E, int dtype, wsf_stream_t stream) {
+    if (!valid_dtype(dtype)) return WSF_ERR_BAD_DTYPE;
+    if (renormalize != 0 && renormalize != 1) return WSF_ERR_BAD_ARG;
+    const int es = elt_bytes(dtype);
+    int64_t lb, db;
+    int rc = router_sizes(T, E, k, ld, es, &lb);
+    if (rc == WSF_OK) rc = router_sizes(T, E, k, ldd, es, &db);
+    if (rc != WSF_OK) return rc;
+    if (T == 0) return WSF_OK;
+    if (!logits || !ids || !counts || !dlogits) return WSF_ERR_NULL_PTR;
+    if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !aligned_to(ids, 4) ||
+        !aligned_to(counts, 4) || !aligned_to(dgates, 4) || !aligned_to(dloss, 4))
+        return WSF_ERR_MISALIGNED;
+    const Span ins[5] = {span(logits, lb), span(ids, T * k * 4), span(counts, E * 4),
+                         span(dgates, dgates ? T * k * 4 : 0), span(dloss, dloss ? 4 : 0)};
+    const Span out = span(dlogits, db);
+    if (clash(&out, 1, ins, 5)) return WSF_ERR_OVERLAP;
+    return cuda_status(wsf::launch_router_bwd(logits, ld, ids, counts, k, renormalize, dgates,
+                                              dloss, dlogits, ldd, T, E, dtype,
+                                              (cudaStream_t)stream));
+}
+
+size_t groupnorm_fwd_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
+    if (!valid_dtype(dtype) || !groupnorm_sizes(N, S, C, G, dtype)) return SIZE_MAX;
+    return (size_t)wsf::groupnorm_fwd_floats(N, S, C, G, dtype) * 4;
+}
+
+int groupnorm_fwd(const void* x, int64_t x_n, int64_t x_s, const float* w, const float* b,
+                  float eps, int act, void* y, int64_t y_n, int64_t y_s, float* mean, float* rstd,
+                  void* workspace, size_t workspace_bytes, int64_t N, int64_t S, int64_t C,
+                  int64_t G, int dtype, wsf_stream_t stream) {
+    if (!valid_dtype(dtype)) return WSF_ERR_BAD_DTYPE;
+    if (!groupnorm_sizes(N, S, C, G, dtype)) return WSF_ERR_BAD_SHAPE;
+    if (!(eps >= 0.0f && eps <= 3.0e38f) || (act != WSF_ACT_NONE && act != WSF_ACT_SILU))
+        return WSF_ERR_BAD_ARG;
+    const int es = elt_bytes(dtype);
+    const Tensor tx = rows_of(x, x_n, x_s, N, S, C, es), ty = rows_of(y, y_n, y_s, N, S, C, es);
+    const bool some = !tx.empty();
+    if (some && (tx.negative() || ty.negative() || (S > 1 && x_s < C) || !ty.distinct()))
+        return WSF_ERR_BAD_STRIDE;
+    if (tx.extent() < 0 || ty.extent() < 0) return WSF_ERR_BAD_SHAPE;
+    const bool stats = N > 0 && C > 0;
+    if ((some && (!x || !y || !w || !b)) || (stats && (!mean || !rstd))) return WSF_ERR_NULL_PTR;
+    if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(w, 4) || !aligned_to(b, 4) ||
+        !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(workspace, 8))
+        return WSF_ERR_MISALIGNED;
+    const size_t need = groupnorm_fwd_workspace_bytes(N, S, C, G, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WSF_ERR_WORKSPACE;
+    if (!stats) return WSF_OK;
+    const Span ins[3] = {tx.bytes(), span(w, some ? C * 4 : 0), span(b, some ? C * 4 : 0)};
+    const Span outs[4] = {ty.bytes(), span(mean, N * G * 4), span(rstd, N * G * 4),
+                          span(workspace, (int64_t)need)};
+    if (clash(outs, 4, ins, 3)) return WSF_ERR_OVERLAP;
+    if (!some) {  // no rows: nothing to take a mean of
+        cudaError_t e = cudaMemsetAsync(mean, 0, N * G * 4, (cudaStream_t)stream);
+        if (e == cudaSuccess) e = cudaMemsetAsync(rstd, 0, N * G * 4, (cudaStream_t)stream);
+        return cuda_status(e);
+    }
+    const wsf::GroupNormFwd a{x, x_n, x_s, w, b, eps, act, y, y_n, y_s, mean, rstd,
+                              workspace, N, S, C, G, dtype};
+    return cuda_status(wsf::launch_groupnorm_fwd(a, (cudaStream_t)stream));
+}
+
+size_t groupnorm_bwd_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
+    if (!valid_dtype(dtype) || !groupnorm_sizes(N, S, C, G, dtype)) return SIZE_MAX;
+    return (size_t)wsf::groupnorm_bwd_floats(N, S, C, G, dtype) * 4;
+}
+
+int groupnorm_bwd(const void* x, int64_t x_n, int64_t x_s, const float* w, const float* b,
+                  const float* mean, const float* rstd, const void* dy, int64_t dy_n,
+                  int64_t dy_s, int act, void* dx, int64_t dx_n, int64_t dx_s, float* grad_w,
+                  float* grad_b, int accumulate, void* workspace, size_t workspace_bytes,
+                  int64_t N, int64_t S, int64_t C, int64_t G, int dtype, wsf_stream_t stream) {
+    if (!valid_dtype(dtype)) return WSF_ERR_BAD_DTYPE;
+    if (!groupnorm_sizes(N, S, C, G, dtype)) return WSF_ERR_BAD_SHAPE;
+    if ((accumulate != 0 && accumulate != 1) || (act != WSF_ACT_NONE && act != WSF_ACT_SILU))
+        return WSF_ERR_BAD_ARG;
+    const int es = elt_bytes(dtype);
+    const Tensor tx = rows_of(x, x_n, x_s, N, S, C, es), tg = rows_of(dy, dy_n, dy_s, N, S, C, es);
+    const Tensor td = rows_of(dx, dx_n, dx_s, N, S, C, es);
+    const bool some = !tx.empty();
+    if (some && (tx.negative() || tg.negative() || td.negative() || (S > 1 && x_s < C) ||
+                 (S > 1 && dy_s < C) || !td.distinct()))
+        return WSF_ERR_BAD_STRIDE;
+    if (tx.extent() < 0 || tg.extent() < 0 || td.extent() < 0) return WSF_ERR_BAD_SHAPE;
+    if ((some && (!x || !dy || !dx || !w || !b || !mean || !rstd)) ||
+        (C > 0 && (!grad_w || !grad_b)))
+        return WSF_ERR_NULL_PTR;
+    if (!aligned_to(x, es) || !aligned_to(dy, es) || !aligned_to(dx, es) || !aligned_to(w, 4) ||
+        !aligned_to(b, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) ||
+        !aligned_to(grad_w, 4) || !aligned_to(grad_b, 4) || !aligned_to(workspace, 8))
+        return WSF_ERR_MISALIGNED;
+    const size_t need = groupnorm_bwd_workspace_bytes(N, S, C, G, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return WSF_ERR_WORKSPACE;
+    if (C == 0) return WSF_OK;
+    const int64_t cb = some ? C * 4 : 0, gb = some ? N * G * 4 : 0;
+    const Span ins[6] = {tx.bytes(), tg.bytes(), span(w, cb), span(b, cb), span(mean, gb),
+                         span(rstd, gb)};
+    const Span outs[4] = {td.bytes(), span(grad_w, C * 4), span(grad_b, C * 4),
+                          span(workspace, (int64_t)need)};
+    if (clash(outs, 4, ins, 6)) return WSF_ERR_OVERLAP;
+    const wsf::GroupNormBwd a{x, x_n, x_s, w, b, mean, rstd, dy, dy_n, dy_s, act, dx, dx_n, dx_s,
+                              grad_w, grad_b, accumulate, workspace, N, S, C, G, dtype};
+    return cuda_status(wsf::launch_groupnorm_bwd(a, (cudaStream_t)stream));
+}
+
+}  // extern "C"

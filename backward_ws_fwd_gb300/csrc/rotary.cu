@@ -1,0 +1,351 @@
+// rotary.cu — rotary positions for the query and key heads of a token
+// (sm_103a), forward and vector-Jacobian product.
+//
+//   θ = position · inv_freq[i],  i < R/2
+//   y_a = s·(x_a cos θ − x_b sin θ),   y_b = s·(x_b cos θ + x_a sin θ)
+//
+// over the pairs (a, b) = (i, i + R/2) or (2i, 2i + 1) of a head's first R
+// elements; the others are copied.  The map is linear in x, so its VJP is
+// the same kernel with sin θ negated.
+//
+// Angles.  position·inv_freq needs more bits than binary32 has once the
+// position passes a few thousand, and binary64 multiplies are slow on this
+// chip.  Only the angle's fraction of a full turn matters, so it is formed in
+// integers: a frequency becomes F = frac(inv_freq / 2π)·2⁶⁴ (freq_turns: one
+// 24 x 64-bit product, exact but for the constant's last bit), and
+// position·F mod 2⁶⁴ is the fraction of a turn, wrapping by itself, for
+// positions of either sign.  Its error is position·2⁻⁶⁴ turns, and the 32
+// bits kept add 2⁻³² turn (1.5e-9 rad).  cos and sin come from Taylor's
+// series on the nearest eighth of a turn (turn_sincos).
+//
+// Bound: HBM (2·es bytes and 3 flops an element).  A block computes the
+// angles of its tokens once into shared memory, while its first loads are in
+// flight, and every head of the token reads them there: without it a
+// 40-head token would evaluate each angle 40 times.
+#include <stdint.h>
+
+#include "wsf_block.h"
+#include "wsf_device.cuh"
+#include "wsf_internal.h"
+
+namespace wsf {
+namespace {
+
+constexpr int NT = 256;
+
+// n / d for 0 <= n < 2^31 and 1 <= d < 2^31 by a multiplication: with
+// l = ceil(log2 d) and m = ceil(2^(31+l) / d) the error of m is below
+// 2^l / 2^(31+l) per unit of n, so floor(n·m / 2^(31+l)) is exact.
+struct FastDiv {
+    uint32_t d, m, sh;  // sh = l - 1; m == 0 stands for d == 1
+};
+
+FastDiv fast_div(uint32_t d) {
+    FastDiv f{d, 0, 0};
+    if (d <= 1) return f;
+    int l = 0;
+    while ((1ull << l) < d) l++;
+    f.m = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
+    f.sh = l - 1;
+    return f;
+}
+
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const FastDiv& f) {
+    return f.m ? __umulhi(n, f.m) >> f.sh : n;
+}
+
+struct View {
+    const char* src;
+    char* dst;
+    long long src_b, src_s, src_h, dst_b, dst_s, dst_h;
+};
+
+struct Params {
+    View v[2];
+    const void* pos;
+    long long ld_pos;
+    const float* inv_freq;
+    float scale, sign;
+    uint32_t tokens, S, Hq, half;  // half = R / 2
+    uint32_t tt;                   // tokens of a block
+    uint32_t pair_items;           // items of a head that hold pairs
+    uint32_t tail;                 // element the copied items start at
+    FastDiv by_s, by_token, by_head;  // token -> batch; item -> token, head
+    int pos64;
+};
+
+// frac(f / 2π)·2⁶⁴ of a finite f, as a wrapping integer.  With f = m·2^(e-150)
+// and C = 2⁶⁶/2π rounded to 64 bits, it is m·C·2^(e-152).
+__device__ __forceinline__ uint64_t freq_turns(float f) {
+    const uint32_t b = __float_as_uint(f);
+    const uint32_t e = (b >> 23) & 255u;
+    const uint64_t m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+    constexpr uint64_t C = 0xa2f9836e4e44152aull;
+    const uint64_t lo = m * C, hi = __umul64hi(m, C);
+    const int sh = 152 - (int)(e ? e : 1u);
+    uint64_t t;
+    if (sh >= 88)
+        t = 0;  // below 2⁻⁶⁴ turn a token
+    else if (sh >= 64)
+        t = hi >> (sh - 64);
+    else if (sh > 0)
+        t = (hi << (64 - sh)) | (lo >> sh);
+    else
+        t = lo << -sh;
+    return b >> 31 ? 0ull - t : t;
+}
+
+// cos and sin of t·2⁻³² turns.  The nearest quarter turn is taken off in
+// integers; on what is left, |a| <= π/4, the series' first dropped terms are
+// a¹¹/11! < 1.8e-9 and a¹²/12! < 1.2e-10.
+__device__ __forceinline__ float2 turn_sincos(uint32_t t) {
+    const uint32_t q = (t + 0x20000000u) >> 30;
+    const float a = (float)(int32_t)(t - (q << 30)) * 1.4629180792671596e-9f;  // 2π·2⁻³²
+    const float z = a * a;
+    float s = fmaf(z, 2.7557319e-6f, -1.9841270e-4f);
+    s = fmaf(z, s, 8.3333333e-3f);
+    s = fmaf(z, s, -1.6666667e-1f);
+    s = fmaf(z * a, s, a);
+    float c = fmaf(z, -2.7557319e-7f, 2.4801587e-5f);
+    c = fmaf(z, c, -1.3888889e-3f);
+    c = fmaf(z, c, 4.1666667e-2f);
+    c = fmaf(z, c, -0.5f);
+    c = fmaf(z, c, 1.0f);
+    const bool swap = q & 1u;
+    float co = swap ? s : c, si = swap ? c : s;
+    if (q == 1u || q == 2u) co = -co;
+    if (q & 2u) si = -si;
+    return make_float2(co, si);
+}
+
+// W elements of T moved in one access.
+template <typename T, int W>
+struct alignas(sizeof(T) * W) Pack {
+    T v[W];
+};
+
+template <int Bytes>
+struct Word;
+template <>
+struct Word<16> { using type = uint4; };
+template <>
+struct Word<8> { using type = uint2; };
+template <>
+struct Word<4> { using type = uint32_t; };
+template <>
+struct Word<2> { using type = unsigned short; };
+
+// Not the read-only path: a call in place reads what it writes.
+template <typename T, int W>
+__device__ __forceinline__ Pack<T, W> get(const T* p) {
+    using U = typename Word<sizeof(T) * W>::type;
+    const U u = __ldcs(reinterpret_cast<const U*>(p));
+    Pack<T, W> r;
+    memcpy(&r, &u, sizeof(U));
+    return r;
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void put(T* p, const Pack<T, W>& r) {
+    using U = typename Word<sizeof(T) * W>::type;
+    U u;
+    memcpy(&u, &r, sizeof(U));
+    __stcs(reinterpret_cast<U*>(p), u);
+}
+
+template <typename T>
+__device__ __forceinline__ T narrow1(float v) {
+    if constexpr (sizeof(T) == 4)
+        return v;
+    else {
+        T t;
+        Elt<T>::store1(&t, v);
+        return t;
+    }
+}
+
+// One item of a head: W pairs (half layout, or W == 1), W/2 pairs
+// (interleaved, W > 1), or, behind the rotated part, W elements to copy.
+// U items of a thread are in flight at a time.
+template <typename T, int W, bool Inter>
+__global__ void __launch_bounds__(NT) rotary_kernel(const __grid_constant__ Params p) {
+    constexpr bool Two = !Inter || W == 1;         // two accesses a pair item
+    constexpr int PW = Two ? W : W / 2;            // pairs of an item
+    constexpr int UN = PW >= 2 ? 2 : 1;            // pairs of a shared-memory unit
+    constexpr int U = Two ? 4 : 8;
+    extern __shared__ float4 smem[];
+    // angles: unit m of item c of token t at ((t·PW/UN + m)·pair_items + c)·UN
+    // pairs, so that neighbouring items read neighbouring units
+    float2* cs = reinterpret_cast<float2*>(smem);
+    const uint32_t pairs = p.pair_items * PW;      // == R / 2
+    long long* base = reinterpret_cast<long long*>(cs + ((size_t)p.tt * pairs + 1) / 2 * 2);
+
+    pdl_wait();
+    const uint32_t tok0 = blockIdx.x * p.tt;
+    const uint32_t nt = min(p.tt, p.tokens - tok0);
+    // element offsets of each token in the four tensors
+    for (uint32_t i = threadIdx.x; i < nt * 4; i += NT) {
+        const uint32_t t = tok0 + i / 4, b = quotient(t, p.by_s), s = t - b * p.S;
+        const View& v = p.v[(i >> 1) & 1];
+        base[i] = i & 1 ? b * v.dst_b + s * v.dst_s : b * v.src_b + s * v.src_s;
+    }
+    for (uint32_t i = threadIdx.x; i < nt * pairs; i += NT) {
+        const uint32_t t = i / pairs, j = i - t * pairs;
+        const uint32_t tok = tok0 + t, b = quotient(tok, p.by_s), s = tok - b * p.S;
+        const long long at = b * p.ld_pos + s;
+        const long long pos = p.pos64 ? __ldg((const long long*)p.pos + at)
+                                      : (long long)__ldg((const int*)p.pos + at);
+        const float f = __ldg(p.inv_freq + j);
+        // a frequency that is not finite gives NaN
+        const float amp = fabsf(f) <= 3.402823466e38f ? p.scale : __int_as_float(0x7fc00000);
+        const float2 r = turn_sincos((uint32_t)(((uint64_t)pos * freq_turns(f)) >> 32));
+        const uint32_t c = j / PW, e = j % PW;
+        cs[((t * (PW / UN) + e / UN) * p.pair_items + c) * UN + e % UN] =
+            make_float2(r.x * amp, r.y * amp * p.sign);
+    }
+    __syncthreads();
+
+    const uint32_t items = nt * p.by_token.d;
+    for (uint32_t i0 = threadIdx.x; i0 < items; i0 += NT * U) {
+        Pack<T, W> a[U], b[Two ? U : 1];
+        T* dst[U];
+        uint32_t tc[U];  // token and item of the head, or a mark
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const uint32_t i = i0 + u * NT;
+            if (i < items) {
+                const uint32_t t = quotient(i, p.by_token), r = i - t * p.by_token.d;
+                uint32_t h = quotient(r, p.by_head);
+                const uint32_t c = r - h * p.by_head.d;
+                const uint32_t w = h >= p.Hq;
+                if (w) h -= p.Hq;
+                const View& v = p.v[w];
+                const bool pair = c < p.pair_items;
+                const uint32_t off = pair ? c * (Inter ? 2 * PW : W)
+                                          : p.tail + (c - p.pair_items) * W;
+                const T* src = (const T*)v.src + base[t * 4 + w * 2] + h * v.src_h + off;
+                dst[u] = (T*)v.dst + base[t * 4 + w * 2 + 1] + h * v.dst_h + off;
+                tc[u] = pair ? t * (PW / UN) * p.pair_items + c : ~0u;
+                a[u] = get<T, W>(src);
+                if constexpr (Two)
+                    if (pair) b[u] = get<T, W>(src + (Inter ? 1u : p.half));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (i0 + u * NT >= items) break;
+            if (tc[u] != ~0u) {
+                float2 g[PW];
+#pragma unroll
+                for (int m = 0; m < PW / UN; m++) {
+                    const float2* q = cs + (size_t)(tc[u] + m * p.pair_items) * UN;
+                    if constexpr (UN == 2) {
+                        const float4 q4 = *reinterpret_cast<const float4*>(q);
+                        g[2 * m] = make_float2(q4.x, q4.y);
+                        g[2 * m + 1] = make_float2(q4.z, q4.w);
+                    } else {
+                        g[m] = *q;
+                    }
+                }
+                if constexpr (Two) {
+#pragma unroll
+                    for (int e = 0; e < PW; e++) {
+                        const float x = Elt<T>::widen1(a[u].v[e]), y = Elt<T>::widen1(b[u].v[e]);
+                        a[u].v[e] = narrow1<T>(x * g[e].x - y * g[e].y);
+                        b[u].v[e] = narrow1<T>(y * g[e].x + x * g[e].y);
+                    }
+                    put<T, W>(dst[u] + (Inter ? 1u : p.half), b[u]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < PW; e++) {
+                        const float x = Elt<T>::widen1(a[u].v[2 * e]);
+                        const float y = Elt<T>::widen1(a[u].v[2 * e + 1]);
+                        a[u].v[2 * e] = narrow1<T>(x * g[e].x - y * g[e].y);
+                        a[u].v[2 * e + 1] = narrow1<T>(y * g[e].x + x * g[e].y);
+                    }
+                }
+            }
+            put<T, W>(dst[u], a[u]);
+        }
+    }
+    pdl_trigger();
+}
+
+template <typename T, int W, bool Inter>
+cudaError_t start(Params& p, int64_t D, int64_t R, int64_t H, bool copy_tail, cudaStream_t s) {
+    p.pair_items = (uint32_t)(R / (Inter && W > 1 ? W : 2 * W));
+    p.tail = (uint32_t)R;
+    const uint32_t per_head = p.pair_items + (copy_tail ? (uint32_t)((D - R) / W) : 0u);
+    if (per_head == 0) return cudaSuccess;  // in place, nothing rotated
+    p.by_head = fast_div(per_head);
+    p.by_token = fast_div(per_head * (uint32_t)H);
+    p.by_s = fast_div(p.S);
+    // Tokens of a block: as many as leave eight blocks an SM, so that the
+    // angles and the block's start are spread over more items.
+    p.tt = 1;
+    while (p.tt < 16 && (int64_t)p.tokens >= (int64_t)p.tt * 2 * kDesignSMs * 8 &&
+           (int64_t)p.tt * 2 * R * 4 <= 32768)
+        p.tt *= 2;
+    const size_t smem = ((size_t)p.tt * (R / 2) + 1) / 2 * 16 + (size_t)p.tt * 32;
+    return launch(rotary_kernel<T, W, Inter>, dim3((p.tokens + p.tt - 1) / p.tt), dim3(NT), smem, s,
+                  true, p);
+}
+
+template <typename T, int W>
+cudaError_t start_layout(Params& p, int64_t D, int64_t R, int64_t H, bool copy_tail, bool inter,
+                         cudaStream_t s) {
+    return inter ? start<T, W, true>(p, D, R, H, copy_tail, s)
+                 : start<T, W, false>(p, D, R, H, copy_tail, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryHeads& q, const RotaryHeads& k, const void* pos,
+                          int64_t ld_pos, int pos_bytes, const float* inv_freq, float scale,
+                          int interleaved, float sign, int64_t B, int64_t S, int64_t D, int64_t R,
+                          int dtype, cudaStream_t s) {
+    const int64_t H = q.H + k.H;
+    if (B == 0 || S == 0 || H == 0 || D == 0) return cudaSuccess;
+    const int es = elt_bytes(dtype);
+    Params p{};
+    const RotaryHeads* t[2] = {&q, &k};
+    // Widest access that divides every address, the head and the halves.
+    uint64_t bits = (uint64_t)D * es | (uint64_t)(interleaved ? R : R / 2) * es;
+    bool in_place = true;
+    for (int i = 0; i < 2; i++) {
+        const RotaryHeads& h = *t[i];
+        p.v[i] = View{(const char*)h.src, (char*)h.dst, h.src_b, h.src_s, h.src_h,
+                      h.dst_b, h.dst_s, h.dst_h};
+        if (h.H == 0) continue;
+        bits |= (uint64_t)(uintptr_t)h.src | (uint64_t)(uintptr_t)h.dst;
+        if (B > 1) bits |= (uint64_t)(h.src_b | h.dst_b) * es;
+        if (S > 1) bits |= (uint64_t)(h.src_s | h.dst_s) * es;
+        if (h.H > 1) bits |= (uint64_t)(h.src_h | h.dst_h) * es;
+        in_place = in_place && h.src == h.dst;
+    }
+    p.pos = pos;
+    p.ld_pos = ld_pos;
+    p.pos64 = pos_bytes == 8;
+    p.inv_freq = inv_freq;
+    p.scale = scale;
+    p.sign = sign;
+    p.tokens = (uint32_t)(B * S);
+    p.S = (uint32_t)S;
+    p.Hq = (uint32_t)q.H;
+    p.half = (uint32_t)(R / 2);
+    const bool tail = !in_place && D > R, inter = interleaved != 0;
+    const int w = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : es;
+    if (dtype == 0)
+        return w == 16  ? start_layout<float, 4>(p, D, R, H, tail, inter, s)
+               : w == 8 ? start_layout<float, 2>(p, D, R, H, tail, inter, s)
+                        : start_layout<float, 1>(p, D, R, H, tail, inter, s);
+    if (dtype == 1)
+        return w == 16  ? start_layout<__half, 8>(p, D, R, H, tail, inter, s)
+               : w == 8 ? start_layout<__half, 4>(p, D, R, H, tail, inter, s)
+                        : start_layout<__half, 1>(p, D, R, H, tail, inter, s);
+    return w == 16  ? start_layout<__nv_bfloat16, 8>(p, D, R, H, tail, inter, s)
+           : w == 8 ? start_layout<__nv_bfloat16, 4>(p, D, R, H, tail, inter, s)
+                    : start_layout<__nv_bfloat16, 1>(p, D, R, H, tail, inter, s);
+}
+
+}  // namespace wsf

@@ -1,0 +1,79 @@
+// wsf_block.h — host-side interface between the C entry points of the block
+// operators (abi_block.cu) and their launchers (rotary.cu, router.cu,
+// groupnorm.cu).  Not installed; not part of the ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace wsf {
+
+// Heads of one rotary tensor: [B, S, H, D], unit inner stride, the other
+// strides in elements.
+struct RotaryHeads {
+    const void* src;
+    void* dst;
+    int64_t src_b, src_s, src_h;
+    int64_t dst_b, dst_s, dst_h;
+    int64_t H;
+};
+
+constexpr int64_t kRotaryMaxR = 1024;           // rotated elements of a head
+constexpr int64_t kRotaryMaxToken = 1 << 24;    // elements of one token, both tensors
+
+// sign = +1 rotates forward, -1 back (the VJP).
+cudaError_t launch_rotary(const RotaryHeads& q, const RotaryHeads& k, const void* pos,
+                          int64_t ld_pos, int pos_bytes, const float* inv_freq, float scale,
+                          int interleaved, float sign, int64_t B, int64_t S, int64_t D, int64_t R,
+                          int dtype, cudaStream_t s);
+
+// Top-k router.  router_tiles: rows P of the forward's partial sums
+// (workspace: P·E floats, then P·E ints).
+constexpr int64_t kRouterMaxE = 1024, kRouterMaxK = 32;
+int64_t router_tiles(int64_t T, int64_t E);
+cudaError_t launch_router_fwd(const void* logits, int64_t ld, const unsigned char* mask, int64_t k,
+                              int renorm, float* gates, int* ids, int* counts, float* loss,
+                              void* workspace, int64_t T, int64_t E, int dtype, cudaStream_t s);
+cudaError_t launch_router_bwd(const void* logits, int64_t ld, const int* ids, const int* counts,
+                              int64_t k, int renorm, const float* dgates, const float* dloss,
+                              void* dlogits, int64_t ldd, int64_t T, int64_t E, int dtype,
+                              cudaStream_t s);
+
+// Group norm of [N, S, C]; strides in elements.  *_floats: workspace size.
+constexpr int64_t kGroupNormMaxC = 16384;
+struct GroupNormFwd {
+    const void* x;
+    int64_t x_n, x_s;
+    const float *w, *b;
+    float eps;
+    int act;
+    void* y;
+    int64_t y_n, y_s;
+    float *mean, *rstd;
+    void* workspace;
+    int64_t N, S, C, G;
+    int dtype;
+};
+struct GroupNormBwd {
+    const void* x;
+    int64_t x_n, x_s;
+    const float *w, *b, *mean, *rstd;
+    const void* dy;
+    int64_t dy_n, dy_s;
+    int act;
+    void* dx;
+    int64_t dx_n, dx_s;
+    float *grad_w, *grad_b;
+    int accumulate;
+    void* workspace;
+    int64_t N, S, C, G;
+    int dtype;
+};
+int64_t groupnorm_fwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dtype);
+int64_t groupnorm_bwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dtype);
+// Row tiles of all samples (the launches' grid).
+int64_t groupnorm_units(int64_t N, int64_t S, int64_t C, int64_t G, int dtype);
+cudaError_t launch_groupnorm_fwd(const GroupNormFwd& a, cudaStream_t s);
+cudaError_t launch_groupnorm_bwd(const GroupNormBwd& a, cudaStream_t s);
+
+}  // namespace wsf

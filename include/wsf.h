@@ -5,6 +5,8 @@
  *   weighted sum   y[i] = Σ_d x[i,d]·w[d]           x [N,D], w [D], y [N]
  *   scaled SiLU    y    = w·x·sigmoid(x)            x [n], scalar w
  *   row softmax, RMSNorm and LayerNorm over the rows of x [N,D]
+ *   rotary positions of query and key heads; the top-k router of a mixture of
+ *   experts with its balance loss; group norm with SiLU, channels last
  *
  * Sources (web pages, cited by title and section):
  *   [WS]   "Writing Triton Kernels with Autograd: A Minimal End-to-End
@@ -302,6 +304,113 @@ int layernorm_bwd(const void* x, int64_t ldx, const float* w, const void* dy, in
                   float eps, void* dx, int64_t lddx, float* grad_w, float* grad_b, int accumulate,
                   void* workspace, size_t workspace_bytes, int64_t N, int64_t D, int dtype,
                   wsf_stream_t stream);
+
+/*
+ * rotary_fwd / rotary_bwd — rotary positions of a token's query and key
+ * heads, and the vector-Jacobian product:
+ *   θ = position·inv_freq[i], i < R/2;  the pair (a, b) of a head becomes
+ *   y_a = scale·(x_a·cos θ − x_b·sin θ),  y_b = scale·(x_b·cos θ + x_a·sin θ)
+ * layout WSF_ROTARY_HALF pairs (i, i + R/2), WSF_ROTARY_INTERLEAVED
+ * (2i, 2i + 1); elements R .. D of a head are copied.  The map is linear, so
+ * rotary_bwd takes dy in q/k and writes dx to yq/yk, turning back by θ.
+ * q: [B, S, Hq, D], k: [B, S, Hk, D] in dtype (Hk == 0: no k), any layout of
+ * unit inner stride: q_strides etc. are host arrays {batch, token, head} in
+ * elements (>= 0; an output's elements must not coincide, WSF_ERR_BAD_STRIDE).
+ * R: even, 0..min(D, 1024).  (Hq + Hk)·D <= 2^24, B·S < 2^31.
+ * positions: [B, S], 4- or 8-byte signed integers (position_bytes), unit
+ * stride along S, row stride ld_positions (0: one row for every batch).
+ * inv_freq: [R/2] binary32, radians a token.  The angle is the exact product
+ * position·inv_freq reduced modulo a turn, within 2e-7 rad for positions of up
+ * to 2^40 (a frequency that is not finite gives NaN); products are binary32 and each output is rounded once.
+ * In place: yq may be q itself (same address, same strides), and yk k;
+ * otherwise outputs must not overlap inputs or one another.  Interleaved
+ * views of one packed buffer that share their batch and token strides do not
+ * overlap.
+ */
+#define WSF_ROTARY_HALF 0
+#define WSF_ROTARY_INTERLEAVED 1
+int rotary_fwd(const void* q, const int64_t* q_strides, void* yq, const int64_t* yq_strides,
+               int64_t Hq, const void* k, const int64_t* k_strides, void* yk,
+               const int64_t* yk_strides, int64_t Hk, const void* positions, int64_t ld_positions,
+               int position_bytes, const float* inv_freq, float scale, int layout, int64_t B,
+               int64_t S, int64_t D, int64_t R, int dtype, wsf_stream_t stream);
+int rotary_bwd(const void* dyq, const int64_t* dyq_strides, void* dq, const int64_t* dq_strides,
+               int64_t Hq, const void* dyk, const int64_t* dyk_strides, void* dk,
+               const int64_t* dk_strides, int64_t Hk, const void* positions, int64_t ld_positions,
+               int position_bytes, const float* inv_freq, float scale, int layout, int64_t B,
+               int64_t S, int64_t D, int64_t R, int dtype, wsf_stream_t stream);
+
+/*
+ * router_fwd — top-k routing over E experts with the balance loss.
+ *   p = softmax(logits[t, :]);  ids[t, :] = the k largest logits, largest
+ *   first, equal ones (−0 and +0 are equal) in index order;
+ *   gates[t, j] = p[ids_j], or with renormalize == 1  p[ids_j] / Σ_i p[ids_i];
+ *   counts[e] = rows that chose e;  V = rows that count;
+ *   loss = E · Σ_e (counts[e] / (k·V)) · (Σ_t p[t, e] / V)      (1 if balanced)
+ * logits: [T, E] dtype, row stride ld (>= E).  mask: [T] bytes, 0 leaves the
+ * row out, or NULL.  A row that is left out, and one with no logit above −inf,
+ * does not count: its ids are −1 and its gates 0.  With no row that counts
+ * the loss is 0.  A NaN or +inf logit of a row that counts makes its gates
+ * and the loss NaN; its ids are k different experts.
+ * gates: [T, k] binary32, ids: [T, k] int32, counts: [E] int32, loss: one
+ * binary32, all contiguous.  1 <= k <= min(E, 32), 1 <= E <= 1024,
+ * T·k < 2^31 (WSF_ERR_BAD_SHAPE).  workspace: router_fwd_workspace_bytes
+ * bytes (per-block partial sums, joined in a fixed order: the same bits on every run).
+ */
+size_t router_fwd_workspace_bytes(int64_t T, int64_t E);
+int router_fwd(const void* logits, int64_t ld, const unsigned char* mask, int64_t k,
+               int renormalize, float* gates, int* ids, int* counts, float* loss, void* workspace,
+               size_t workspace_bytes, int64_t T, int64_t E, int dtype, wsf_stream_t stream);
+
+/*
+ * router_bwd — its vector-Jacobian product with the choice held constant:
+ *   a_e = dloss·E·counts[e] / (k·V²),  V = Σ counts / k
+ *   dlogits = p·(a + u − Σ (a + u)·p),  u = dgates at ids, 0 elsewhere, or
+ *   renormalize == 1:  p·(a − Σ a·p) + gates·(u − Σ u·gates)  at ids.
+ * ids, counts: as router_fwd wrote them (a row's ids are distinct; ids of −1
+ * mark a row that does not count, whose dlogits are 0).  Counts summed over
+ * several micro-batches or replicas give the gradient of their common loss.
+ * dgates: [T, k] binary32 or NULL (zeros); dloss: one binary32 or NULL
+ * (zero).  dlogits: [T, E] dtype, row stride ldd.  Sizes as for router_fwd.
+ */
+int router_bwd(const void* logits, int64_t ld, const int* ids, const int* counts, int64_t k,
+               int renormalize, const float* dgates, const float* dloss, void* dlogits,
+               int64_t ldd, int64_t T, int64_t E, int dtype, wsf_stream_t stream);
+
+/*
+ * groupnorm_fwd / groupnorm_bwd — group norm over channels-last values with
+ * an optional SiLU.  x [N, S, C], G groups of C/G consecutive channels; μ and
+ * r = 1/sqrt(var + eps) over the S·C/G values of a group of a sample:
+ *   x̂ = (x − μ)·r,  z = x̂·w + b,  y = z (WSF_ACT_NONE) or z·sigmoid(z)
+ *   (WSF_ACT_SILU);  mean, rstd: μ and r, [N, G] binary32
+ * and, with dz = dy or dy·silu′(z), g = dz·w, means over a group:
+ *   dx = r·(g − mean g − x̂·mean(g·x̂)),
+ *   grad_w[c] = Σ_{n,s} dz·x̂,  grad_b[c] = Σ_{n,s} dz.
+ * S == 1 is the norm of a token's heads; S = H·W that of feature maps.
+ * x, y, dy, dx: dtype, unit stride along C, strides x_n (sample) and x_s
+ * (row, >= C) in elements.  w, b, grad_w, grad_b: [C] binary32.
+ * C <= 16384, C % G == 0 (WSF_ERR_BAD_SHAPE), eps finite and >= 0.  The
+ * statistics are kept for the backward, which would otherwise read x once
+ * more than it has to (a group does not fit one block, unlike a row of
+ * layernorm_bwd); arithmetic is binary32, each output rounded once.
+ * The parameter gradients are summed in a fixed order and added to the
+ * existing values when accumulate == 1.  N == 0 or S == 0 gives zero
+ * gradients (or leaves them when accumulating) and, S == 0, zero mean and
+ * rstd; C == 0 does nothing.  Workspace: the *_workspace_bytes queries.
+ */
+#define WSF_ACT_NONE 0
+#define WSF_ACT_SILU 1
+size_t groupnorm_fwd_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int dtype);
+int groupnorm_fwd(const void* x, int64_t x_n, int64_t x_s, const float* w, const float* b,
+                  float eps, int act, void* y, int64_t y_n, int64_t y_s, float* mean, float* rstd,
+                  void* workspace, size_t workspace_bytes, int64_t N, int64_t S, int64_t C,
+                  int64_t G, int dtype, wsf_stream_t stream);
+size_t groupnorm_bwd_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int dtype);
+int groupnorm_bwd(const void* x, int64_t x_n, int64_t x_s, const float* w, const float* b,
+                  const float* mean, const float* rstd, const void* dy, int64_t dy_n,
+                  int64_t dy_s, int act, void* dx, int64_t dx_n, int64_t dx_s, float* grad_w,
+                  float* grad_b, int accumulate, void* workspace, size_t workspace_bytes,
+                  int64_t N, int64_t S, int64_t C, int64_t G, int dtype, wsf_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,269 @@
+"""Host-only checks of the block operators' entry points (rotary, router,
+group norm): every refusal of include/wsf.h, before any device is touched.
+Pointers are fake addresses that are never dereferenced."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+F = 0x10000000
+
+
+@pytest.fixture(scope="module")
+def wsf():
+    import __graft_entry__
+    __graft_entry__._cuda_build_module().build()
+    import backward_ws_fwd_gb300 as m
+    return m
+
+
+def _p(a):
+    return None if a is None else ctypes.c_void_p(a)
+
+
+def _s(*v):
+    return (ctypes.c_int64 * 3)(*v)
+
+
+def rotary(wsf, **over):
+    a = dict(q=F, qs=(8 * 512, 512, 64), yq=2 * F, yqs=(8 * 512, 512, 64), Hq=8,
+             k=3 * F, ks=(8 * 128, 128, 64), yk=4 * F, yks=(8 * 128, 128, 64), Hk=2,
+             pos=5 * F, ld=8, pb=8, f=6 * F, scale=1.0, layout=0, B=2, S=8, D=64, R=64, dt=wsf.BF16)
+    a.update(over)
+    st = {n: None if a[n] is None else _s(*a[n]) for n in ("qs", "yqs", "ks", "yks")}
+    for fn in (wsf.lib.rotary_fwd, wsf.lib.rotary_bwd):
+        rc = fn(_p(a["q"]), st["qs"], _p(a["yq"]), st["yqs"], a["Hq"], _p(a["k"]), st["ks"],
+                _p(a["yk"]), st["yks"], a["Hk"], _p(a["pos"]), a["ld"], a["pb"], _p(a["f"]),
+                a["scale"], a["layout"], a["B"], a["S"], a["D"], a["R"], a["dt"], None)
+    return rc
+
+
+def test_rotary_rejects(wsf):
+    r = lambda **o: rotary(wsf, **o)  # noqa: E731
+    assert r(dt=5) == wsf.ERR_BAD_DTYPE
+    for o in (dict(B=-1), dict(S=-1), dict(D=-1), dict(Hq=-1), dict(Hk=-1), dict(R=-2), dict(R=63),
+              dict(R=66), dict(D=2048, R=1026), dict(B=1 << 20, S=1 << 12), dict(Hq=1 << 20),
+              dict(Hq=1 << 62), dict(qs=(1 << 62, 512, 64))):
+        assert r(**o) == wsf.ERR_BAD_SHAPE, o
+    for o in (dict(pb=2), dict(layout=2), dict(scale=math.inf), dict(scale=math.nan)):
+        assert r(**o) == wsf.ERR_BAD_ARG, o
+    for n in ("q", "yq", "k", "yk", "pos", "f", "qs", "yqs", "ks", "yks"):
+        assert r(**{n: None}) == wsf.ERR_NULL_PTR, n
+    # outputs whose elements coincide, negative strides, positions of other rows
+    for o in (dict(yqs=(8 * 512, 512, 32)), dict(yqs=(0, 512, 64)), dict(yqs=(8 * 512, 64, 64)),
+              dict(yks=(8 * 128, 100, 64)), dict(qs=(8 * 512, -512, 64)), dict(ld=7), dict(ld=-8)):
+        assert r(**o) == wsf.ERR_BAD_STRIDE, o
+    for o in (dict(q=F + 1), dict(yk=4 * F + 1), dict(pos=5 * F + 4), dict(f=6 * F + 2)):
+        assert r(**o) == wsf.ERR_MISALIGNED, o
+    # overlaps: shifted in place, q's output on k, outputs on one another or on positions
+    for o in (dict(yq=F + 128), dict(yq=3 * F), dict(yk=2 * F), dict(yq=5 * F - 1024), dict(yk=6 * F),
+              dict(yq=F, yqs=(8 * 512, 64, 512))):
+        assert r(**o) == wsf.ERR_OVERLAP, o
+    # nothing to do
+    for o in (dict(B=0), dict(S=0), dict(D=0, R=0), dict(Hq=0, Hk=0)):
+        assert r(**o) == wsf.OK, o
+
+
+def test_rotary_packed_views(wsf):
+    """Views of q and k in one packed buffer [B, S, Hq + 2 Hk, D], in place:
+    the refusals (the accepted call is made on a GPU)."""
+    H, D = 12, 64
+    st = (8 * H * D, H * D, D)
+    q, k = F, F + 8 * D * 2
+    base = dict(qs=st, yqs=st, ks=st, yks=st)
+    # v's heads start where k's end: a k output one head too far to the left meets q's
+    assert rotary(wsf, q=q, yq=q, k=k, yk=k - D * 2, **base) == wsf.ERR_OVERLAP
+    assert rotary(wsf, q=q, yq=q + 2 * D * 2, k=k, yk=k, **base) == wsf.ERR_OVERLAP
+    # another period: cannot be told apart
+    other = (8 * H * D, 2 * H * D, D)
+    assert rotary(wsf, q=q, yq=q, k=k, yk=k, **{**base, "ks": other, "yks": other}) in (
+        wsf.ERR_OVERLAP, wsf.ERR_BAD_STRIDE)
+
+
+def router_fwd(wsf, **over):
+    a = dict(l=F, ld=64, mask=None, k=8, renorm=0, gates=2 * F, ids=3 * F, counts=4 * F,
+             loss=5 * F, ws=6 * F, wb=1 << 30, T=100, E=64, dt=wsf.BF16)
+    a.update(over)
+    return wsf.lib.router_fwd(_p(a["l"]), a["ld"], _p(a["mask"]), a["k"], a["renorm"], _p(a["gates"]),
+                              _p(a["ids"]), _p(a["counts"]), _p(a["loss"]), _p(a["ws"]), a["wb"],
+                              a["T"], a["E"], a["dt"], None)
+
+
+def test_router_fwd_rejects(wsf):
+    r = lambda **o: router_fwd(wsf, **o)  # noqa: E731
+    assert r(dt=3) == wsf.ERR_BAD_DTYPE
+    for o in (dict(T=-1), dict(E=0), dict(E=1025, ld=2000), dict(k=0), dict(k=33), dict(E=4, k=5),
+              dict(T=1 << 30), dict(ld=1 << 60)):
+        assert r(**o) == wsf.ERR_BAD_SHAPE, o
+    assert r(renorm=2) == wsf.ERR_BAD_ARG
+    assert r(ld=63) == wsf.ERR_BAD_STRIDE
+    for n in ("l", "gates", "ids", "counts", "loss"):
+        assert r(**{n: None}) == wsf.ERR_NULL_PTR, n
+    for o in (dict(l=F + 1), dict(gates=2 * F + 2), dict(ids=3 * F + 1), dict(counts=4 * F + 2),
+              dict(loss=5 * F + 1), dict(ws=6 * F + 2)):
+        assert r(**o) == wsf.ERR_MISALIGNED, o
+    need = wsf.router_fwd_workspace_bytes(100, 64)
+    assert need > 0
+    assert r(wb=need - 1) == wsf.ERR_WORKSPACE and r(ws=None) == wsf.ERR_WORKSPACE
+    for o in (dict(gates=F), dict(ids=F + 4), dict(counts=3 * F), dict(loss=2 * F), dict(ws=3 * F),
+              dict(mask=2 * F), dict(loss=4 * F + 4)):
+        assert r(**o) == wsf.ERR_OVERLAP, o
+
+
+def test_router_bwd_rejects(wsf):
+    a0 = dict(l=F, ld=64, ids=2 * F, counts=3 * F, k=8, renorm=0, dg=4 * F, dl=5 * F, out=6 * F,
+              ldd=64, T=100, E=64, dt=wsf.BF16)
+
+    def r(**o):
+        a = {**a0, **o}
+        return wsf.lib.router_bwd(_p(a["l"]), a["ld"], _p(a["ids"]), _p(a["counts"]), a["k"],
+                                  a["renorm"], _p(a["dg"]), _p(a["dl"]), _p(a["out"]), a["ldd"],
+                                  a["T"], a["E"], a["dt"], None)
+
+    assert r(dt=-1) == wsf.ERR_BAD_DTYPE
+    assert r(E=0) == r(k=0) == r(T=-1) == r(k=33) == wsf.ERR_BAD_SHAPE
+    assert r(renorm=-1) == wsf.ERR_BAD_ARG
+    assert r(ld=60) == r(ldd=63) == wsf.ERR_BAD_STRIDE
+    for n in ("l", "ids", "counts", "out"):
+        assert r(**{n: None}) == wsf.ERR_NULL_PTR, n
+    assert r(out=6 * F + 1) == r(dg=4 * F + 2) == r(dl=5 * F + 1) == wsf.ERR_MISALIGNED
+    for o in (dict(out=F), dict(out=2 * F), dict(out=3 * F - 128), dict(out=4 * F), dict(out=5 * F)):
+        assert r(**o) == wsf.ERR_OVERLAP, o
+    assert r(T=0) == wsf.OK
+
+
+def gn_fwd(wsf, **over):
+    a = dict(x=F, xn=320 * 16, xs=320, w=2 * F, b=3 * F, eps=1e-5, act=1, y=4 * F, yn=320 * 16, ys=320,
+             mean=5 * F, rstd=6 * F, ws=7 * F, wb=1 << 30, N=4, S=16, C=320, G=32, dt=wsf.F16)
+    a.update(over)
+    return wsf.lib.groupnorm_fwd(_p(a["x"]), a["xn"], a["xs"], _p(a["w"]), _p(a["b"]), a["eps"],
+                                 a["act"], _p(a["y"]), a["yn"], a["ys"], _p(a["mean"]),
+                                 _p(a["rstd"]), _p(a["ws"]), a["wb"], a["N"], a["S"], a["C"],
+                                 a["G"], a["dt"], None)
+
+
+def test_groupnorm_fwd_rejects(wsf):
+    r = lambda **o: gn_fwd(wsf, **o)  # noqa: E731
+    assert r(dt=4) == wsf.ERR_BAD_DTYPE
+    for o in (dict(N=-1), dict(S=-1), dict(C=-320), dict(G=0), dict(G=-1), dict(G=33),
+              dict(C=16416, G=32), dict(N=1 << 40), dict(S=1 << 55), dict(xn=1 << 62)):
+        assert r(**o) == wsf.ERR_BAD_SHAPE, o
+    for o in (dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(act=2), dict(act=-1)):
+        assert r(**o) == wsf.ERR_BAD_ARG, o
+    for o in (dict(xs=319), dict(ys=319), dict(yn=0), dict(yn=320 * 15), dict(xn=-1)):
+        assert r(**o) == wsf.ERR_BAD_STRIDE, o
+    for n in ("x", "w", "b", "y", "mean", "rstd"):
+        assert r(**{n: None}) == wsf.ERR_NULL_PTR, n
+    for o in (dict(x=F + 1), dict(y=4 * F + 1), dict(w=2 * F + 2), dict(b=3 * F + 1),
+              dict(mean=5 * F + 2), dict(rstd=6 * F + 2), dict(ws=7 * F + 4)):
+        assert r(**o) == wsf.ERR_MISALIGNED, o
+    need = wsf.groupnorm_workspace_bytes(4, 16, 320, 32, wsf.F16, False)
+    if need:
+        assert r(wb=need - 1) == wsf.ERR_WORKSPACE and r(ws=None) == wsf.ERR_WORKSPACE
+    for o in (dict(y=F), dict(y=2 * F), dict(y=3 * F - 64), dict(mean=F), dict(rstd=5 * F),
+              dict(mean=4 * F)):
+        assert r(**o) == wsf.ERR_OVERLAP, o
+    assert r(N=0) == r(C=0) == wsf.OK
+
+
+def test_groupnorm_bwd_rejects(wsf):
+    a0 = dict(x=F, xn=320 * 16, xs=320, w=2 * F, b=3 * F, mean=4 * F, rstd=5 * F, dy=6 * F,
+              gn=320 * 16, gs=320, act=1, dx=7 * F, dn=320 * 16, ds=320, gw=8 * F, gb=9 * F, acc=0,
+              ws=10 * F, wb=1 << 30, N=4, S=16, C=320, G=32, dt=wsf.F32)
+
+    def r(**o):
+        a = {**a0, **o}
+        return wsf.lib.groupnorm_bwd(_p(a["x"]), a["xn"], a["xs"], _p(a["w"]), _p(a["b"]),
+                                     _p(a["mean"]), _p(a["rstd"]), _p(a["dy"]), a["gn"], a["gs"],
+                                     a["act"], _p(a["dx"]), a["dn"], a["ds"], _p(a["gw"]),
+                                     _p(a["gb"]), a["acc"], _p(a["ws"]), a["wb"], a["N"], a["S"],
+                                     a["C"], a["G"], a["dt"], None)
+
+    assert r(dt=4) == wsf.ERR_BAD_DTYPE
+    assert r(N=-1) == r(G=7) == r(C=16416) == wsf.ERR_BAD_SHAPE
+    assert r(act=2) == r(acc=2) == wsf.ERR_BAD_ARG
+    assert r(xs=319) == r(gs=1) == r(ds=319) == r(dn=0) == wsf.ERR_BAD_STRIDE
+    for n in ("x", "w", "b", "mean", "rstd", "dy", "dx", "gw", "gb"):
+        assert r(**{n: None}) == wsf.ERR_NULL_PTR, n
+    for n in ("x", "w", "b", "mean", "rstd", "dy", "dx", "gw", "gb", "ws"):
+        assert r(**{n: a0[n] + 2}) == wsf.ERR_MISALIGNED, n
+    need = wsf.groupnorm_workspace_bytes(4, 16, 320, 32, wsf.F32, True)
+    assert need > 0
+    assert r(wb=need - 1) == wsf.ERR_WORKSPACE and r(ws=None) == wsf.ERR_WORKSPACE
+    for o in (dict(dx=F), dict(dx=6 * F), dict(gw=2 * F), dict(gb=8 * F), dict(gw=4 * F + 64),
+              dict(ws=7 * F), dict(gw=10 * F)):
+        assert r(**o) == wsf.ERR_OVERLAP, o
+    assert r(C=0, G=1) == wsf.OK
+
+
+def test_workspace_queries(wsf):
+    assert wsf.router_fwd_workspace_bytes(0, 64) == 0
+    assert wsf.router_fwd_workspace_bytes(-1, 64) == wsf.SIZE_MAX
+    assert wsf.router_fwd_workspace_bytes(5, 2000) == wsf.SIZE_MAX
+    # bounded whatever the rows: 608 blocks of partial sums and counts
+    assert wsf.router_fwd_workspace_bytes(1 << 24, 256) <= 608 * 256 * 8
+    q = wsf.groupnorm_workspace_bytes
+    assert q(0, 5, 64, 8, torch.float16, True) == 0 == q(3, 0, 64, 8, torch.float16, False)
+    assert q(3, 5, 64, 7, torch.float16, True) == wsf.SIZE_MAX
+
+
+def test_binding_refuses_what_the_library_cannot_see(wsf):
+    """Shapes and types, on the host (no tensor reaches the device)."""
+    q, k = torch.zeros(2, 8, 4, 64), torch.zeros(2, 8, 2, 64)
+    pos, f = torch.zeros(2, 8, dtype=torch.int64), torch.ones(32)
+    bad = [(q, k[:1], pos, f), (q, k[..., :32], pos, f), (q, k, pos[:, :7], f), (q, k, pos.float(), f),
+           (q, k, pos, f.double()), (q, k.half(), pos, f), (q[0, 0], None, pos, f),
+           (q.transpose(2, 3), None, pos, f), (q, k, pos.t().contiguous().t(), f)]
+    for args in bad:
+        for fn in (wsf.rotary_fwd, wsf.rotary_bwd):
+            with pytest.raises((TypeError, ValueError)):
+                fn(*args)
+    l = torch.zeros(10, 8)
+    ids, counts = torch.zeros(10, 2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    dg, dl = torch.zeros(10, 2), torch.zeros(())
+    for kw in (dict(mask=torch.ones(9, dtype=torch.bool)), dict(mask=torch.ones(10)),
+               dict(gates=torch.zeros(10, 3)), dict(ids=ids.long()), dict(loss=torch.zeros(1))):
+        with pytest.raises((TypeError, ValueError)):
+            wsf.router_fwd(l, 2, **kw)
+    for args in ((l, ids.long(), counts, dg, dl), (l, ids, counts[:7], dg, dl), (l, ids, counts, dg[:9], dl),
+                 (l, ids, counts, dg, torch.zeros(1)), (l.t(), ids, counts, dg, dl)):
+        with pytest.raises((TypeError, ValueError)):
+            wsf.router_bwd(*args)
+    x, w = torch.zeros(2, 6, 64), torch.ones(64)
+    st = torch.zeros(2, 8)
+    for args, kw in (((x, w[:63], w, 8), {}), ((x, w, w.half(), 8), {}), ((x[0, 0], w, w, 8), {}),
+                     ((x, w, w, 8), dict(act="gelu")), ((x, w, w, 8), dict(mean=torch.zeros(2, 4)))):
+        with pytest.raises((TypeError, ValueError)):
+            wsf.groupnorm_fwd(*args, **kw)
+    for args in ((x, w, w, st, st, x[:, :5], 8), (x, w, w, st, st, x.half(), 8),
+                 (x, w, w, st[:1], st, x, 8), (x, w, w, st, st, x, 4)):
+        with pytest.raises((TypeError, ValueError)):
+            wsf.groupnorm_bwd(*args)
+
+
+def test_rotary_frequencies(wsf):
+    """Against the definitions, in 64 bits."""
+    f, s = wsf.rotary_frequencies(64)
+    want = [10000.0 ** (-2 * i / 64) for i in range(32)]
+    assert s == 1.0 and f.dtype == torch.float32
+    assert all(abs(a - b) <= 2.0 ** -24 * b for a, b in zip(f.tolist(), want))
+    g, s = wsf.rotary_frequencies(64, scaling="linear", factor=8.0)
+    assert s == 1.0 and all(abs(a - b / 8) <= 2.0 ** -24 * b / 8 for a, b in zip(g.tolist(), want))
+    g, s = wsf.rotary_frequencies(64, scaling="base", factor=8.0)
+    assert s == 1.0 and g[0] == 1.0 and abs(g[-1] - want[-1] / 8) <= 2.0 ** -22 * want[-1] / 8
+    g, s = wsf.rotary_frequencies(64, scaling="parts", factor=8.0, original_length=4096)
+    assert abs(s - (0.1 * math.log(8) + 1)) < 1e-12
+    turns = [4096 * w / (2 * math.pi) for w in want]
+    for a, b, t in zip(g.tolist(), want, turns):
+        if t > 40:
+            assert abs(a - b) <= 2.0 ** -24 * b
+        elif t < 0.9:
+            assert abs(a - b / 8) <= 2.0 ** -24 * b / 8
+        else:
+            assert b / 8 * (1 - 2.0 ** -23) <= a <= b * (1 + 2.0 ** -23)
+    assert wsf.rotary_frequencies(0)[0].numel() == 0
+    for kw in (dict(R=5), dict(R=8, scaling="other"), dict(R=8, scaling="parts", factor=2.0),
+               dict(R=8, factor=0.5), dict(R=8, base=1.0)):
+        with pytest.raises(ValueError):
+            wsf.rotary_frequencies(**kw)

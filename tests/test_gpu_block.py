@@ -1,0 +1,246 @@
+"""The block operators together and through autograd: a transformer block built
+from the library's operators (RMSNorm, rotary positions, softmax attention,
+per-head group norm with SiLU, LayerNorm, top-k router, scaled SiLU experts)
+with its gradients against the same block in 64-bit torch; the autograd glue
+of each operator; a captured training step."""
+import math
+
+import pytest
+import torch
+
+import blockref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def ag():
+    import __graft_entry__
+    __graft_entry__.build()
+    from backward_ws_fwd_gb300 import autograd
+    return autograd
+
+
+def _params(Dm, H, Hk, Dh, E, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def r(*shape, scale=1.0):
+        return torch.randn(*shape, generator=g, device=DEV) * scale
+
+    p = dict(n1=1 + 0.1 * r(Dm), qkv=r((H + 2 * Hk) * Dh, Dm, scale=Dm ** -0.5), gw=1 + 0.1 * r(H * Dh),
+             gb=0.1 * r(H * Dh), o=r(Dm, H * Dh, scale=(H * Dh) ** -0.5), n2=1 + 0.1 * r(Dm), b2=0.1 * r(Dm),
+             router=r(E, Dm, scale=2 * Dm ** -0.5), up=r(E, 2 * Dm, Dm, scale=Dm ** -0.5),
+             down=r(E, Dm, 2 * Dm, scale=(2 * Dm) ** -0.5), ws=torch.full((1,), 0.8, device=DEV))
+    return {k: v.requires_grad_() for k, v in p.items()}
+
+
+def _block(p, x, pos, freq, mask, shape, ops):
+    """One block; ops: the operators, by name."""
+    H, Hk, Dh, E, k = shape
+    B, S, Dm = x.shape
+    h = ops["rms"](x, p["n1"])
+    qkv = (h @ p["qkv"].t()).view(B, S, H + 2 * Hk, Dh)
+    q, kk = ops["rotary"](qkv[:, :, :H], qkv[:, :, H:H + Hk], pos, freq)
+    v = qkv[:, :, H + Hk:]
+    kk, v = (t.repeat_interleave(H // Hk, 2) for t in (kk, v))
+    a = torch.einsum("bshd,bthd->bhst", q, kk) / math.sqrt(Dh)
+    late = torch.ones(S, S, dtype=torch.bool, device=x.device).triu(1)
+    a = ops["softmax"](a.masked_fill(late, -math.inf))
+    o = torch.einsum("bhst,bthd->bshd", a, v).reshape(B * S, H * Dh)
+    o = ops["gn"](o, p["gw"], p["gb"], H)
+    x = x + (o @ p["o"].t()).view(B, S, Dm)
+    h = ops["ln"](x, p["n2"], p["b2"]).reshape(B * S, Dm)
+    gates, ids, counts, balance = ops["router"](h @ p["router"].t(), k, mask)
+    every = torch.einsum("tf,edf->ted", ops["silu"](torch.einsum("td,efd->tef", h, p["up"]).sum(1), p["ws"]),
+                         p["down"])  # a small stand-in for the experts' products
+    take = torch.gather(every, 1, ids.clamp(min=0).long()[:, :, None].expand(-1, -1, Dm))
+    x = x.reshape(B * S, Dm) + (gates[:, :, None] * take).sum(1)
+    return x.view(B, S, Dm), balance, ids, counts
+
+
+def _ops64(freq):
+    def rms(x, w):
+        return x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-5) * w
+
+    def rotary(q, k, pos, f):
+        th = pos.double().reshape(-1, q.shape[1], 1, 1) * f.double()
+        c, s = th.cos(), th.sin()
+
+        def one(x):
+            a, b = x.chunk(2, -1)
+            return torch.cat((a * c - b * s, b * c + a * s), -1)
+
+        return one(q), one(k)
+
+    def gn(x, w, b, G):
+        h = x.view(x.shape[0], G, -1)
+        m = h.mean(-1, keepdim=True)
+        h = (h - m) / torch.sqrt(((h - m) ** 2).mean(-1, keepdim=True) + 1e-5)
+        z = h.view(x.shape) * w + b
+        return z * torch.sigmoid(z)
+
+    def ln(x, w, b):
+        m = x.mean(-1, keepdim=True)
+        return (x - m) / torch.sqrt(((x - m) ** 2).mean(-1, keepdim=True) + 1e-5) * w + b
+
+    def router(l, k, mask):
+        p = torch.softmax(l, 1) * mask[:, None]
+        ids = torch.sort(l, dim=1, descending=True, stable=True)[1][:, :k]
+        g = p.gather(1, ids)
+        g = torch.where(mask[:, None], g / g.sum(1, keepdim=True).clamp(min=1e-300), 0.0)
+        E, V = l.shape[1], mask.sum()
+        counts = torch.zeros(E, device=l.device, dtype=torch.float64)
+        counts.index_add_(0, ids[mask].reshape(-1), torch.ones_like(ids[mask].reshape(-1), dtype=torch.float64))
+        return g, torch.where(mask[:, None], ids, -1), counts, E * (counts / (k * V) * p.sum(0) / V).sum()
+
+    return dict(rms=rms, rotary=rotary, softmax=lambda a: torch.softmax(a, -1), gn=gn, ln=ln, router=router,
+                silu=lambda x, w: w * x * torch.sigmoid(x))
+
+
+def _ops(ag):
+    return dict(rms=ag.rms_norm, rotary=lambda q, k, pos, f: ag.rotary(q, k, pos, f), softmax=ag.softmax,
+                gn=lambda x, w, b, G: ag.group_norm(x, w, b, G, 1e-5, "silu"), ln=ag.layer_norm,
+                router=lambda l, k, mask: ag.topk_router(l, k, mask, True), silu=ag.scaled_silu)
+
+
+def test_a_block_with_its_gradients(ag):
+    """In binary32, every gradient within 2e-4 of the 64-bit block's norm:
+    about 40 operators in a row, each good to some 1e-6, and matrix products
+    in binary32 (torch's, without tf32)."""
+    assert not torch.backends.cuda.matmul.allow_tf32
+    B, S, Dm, H, Hk, Dh, E, k = 2, 24, 64, 4, 2, 32, 8, 2
+    p = _params(Dm, H, Hk, Dh, E)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(B, S, Dm, generator=g, device=DEV).requires_grad_()
+    up = torch.randn(B, S, Dm, generator=g, device=DEV)
+    pos = torch.arange(S, device=DEV) + torch.tensor([[0], [1000]], device=DEV)
+    import backward_ws_fwd_gb300 as wsf
+    freq, _ = wsf.rotary_frequencies(Dh, device=DEV)
+    mask = torch.ones(B * S, dtype=torch.bool, device=DEV)
+    mask[-5:] = False
+    y, bal, ids, counts = _block(p, x, pos, freq, mask, (H, Hk, Dh, E, k), _ops(ag))
+    ((y * up).sum() + 3.0 * bal).backward()
+    p64 = {n: t.detach().double().requires_grad_() for n, t in p.items()}
+    x64 = x.detach().double().requires_grad_()
+    y64, bal64, ids64, _ = _block(p64, x64, pos, freq, mask, (H, Hk, Dh, E, k), _ops64(freq))
+    assert torch.equal(ids.long(), ids64)
+    ((y64 * up.double()).sum() + 3.0 * bal64).backward()
+    assert int(counts.sum()) == k * int(mask.sum())
+    assert float((y.double() - y64).norm() / y64.norm()) <= 1e-5
+    assert abs(float(bal) - float(bal64)) <= 1e-5 * float(bal64)
+    for n, a, b in [("x", x, x64)] + [(n, p[n], p64[n]) for n in p]:
+        assert float((a.grad.double() - b.grad).norm() / b.grad.norm()) <= 2e-4, n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_rotary_autograd(ag, dtype):
+    g = torch.Generator(device=DEV).manual_seed(2)
+    packed = torch.randn(2, 9, 6, 32, generator=g, device=DEV).to(dtype).requires_grad_()
+    pos = torch.arange(9, device=DEV)
+    f = torch.tensor([1.0, 0.3, 0.01, 0.002], device=DEV)
+    yq, yk = ag.rotary(packed[:, :, :4], packed[:, :, 4:5], pos, f, 1.5, True)
+    uq, uk = torch.randn_like(yq), torch.randn_like(yk)
+    torch.autograd.backward((yq, yk), (uq, uk))
+    for u, s in ((uq, slice(0, 4)), (uk, slice(4, 5))):
+        want, tol = ref.rotary(u, pos, f, 1.5, True, -1.0)
+        assert ref.worst(packed.grad[:, :, s], want, tol) <= 1.0
+    assert bool((packed.grad[:, :, 5] == 0).all())
+    # one of the two needs no gradient, k missing, an expanded upstream gradient
+    q = packed.detach()[:, :, :4].requires_grad_()
+    yq, yk = ag.rotary(q, packed.detach()[:, :, 4:5], pos, f)
+    yq.sum().backward()
+    want, tol = ref.rotary(torch.ones_like(q.detach()), pos, f, 1.0, False, -1.0)
+    assert ref.worst(q.grad, want, tol) <= 1.0
+    k = packed.detach()[:, :, 4:5].requires_grad_()
+    _, yk = ag.rotary(packed.detach()[:, :, :4], k, pos, f)
+    yk.sum().backward()
+    assert ref.worst(k.grad, want[:, :, :1], tol[:, :, :1]) <= 1.0
+    one, none = ag.rotary(q, None, pos, f)
+    assert none is None and one.requires_grad
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_router_autograd(ag, renorm):
+    g = torch.Generator(device=DEV).manual_seed(3)
+    l = torch.randn(4, 15, 20, generator=g, device=DEV).requires_grad_()
+    mask = torch.rand(4, 15, generator=g, device=DEV) > 0.2
+    gates, ids, counts, loss = ag.topk_router(l, 3, mask, renorm)
+    assert gates.shape == ids.shape == (4, 15, 3) and not ids.requires_grad and not counts.requires_grad
+    u = torch.randn(4, 15, 3, generator=g, device=DEV)
+    (gates * u).sum().add(loss * 0.7).backward()
+    r = ref.router(l.detach().view(60, 20), 3, mask.view(60), renorm, u.view(60, 3), 0.7)
+    assert ref.worst(l.grad.view(60, 20), r["dlogits"], r["dlogits_tol"]) <= 1.0
+    # the loss alone, the gates alone
+    for pick, dg, dl in ((lambda o: o[3] * 0.7, None, 0.7), (lambda o: (o[0] * u).sum(), u.view(60, 3), 0.0)):
+        x = l.detach().clone().requires_grad_()
+        pick(ag.topk_router(x, 3, mask, renorm)).backward()
+        r = ref.router(l.detach().view(60, 20), 3, mask.view(60), renorm,
+                       torch.zeros(60, 3, device=DEV) if dg is None else dg, dl)
+        assert ref.worst(x.grad.view(60, 20), r["dlogits"], r["dlogits_tol"] + 2.0 ** -149) <= 1.0
+
+
+def test_groupnorm_module(ag):
+    g = torch.Generator(device=DEV).manual_seed(4)
+    m = ag.GroupNorm(4, 64, act="silu", device=DEV)
+    with torch.no_grad():
+        m.weight.add_(0.1 * torch.randn(64, generator=g, device=DEV))
+        m.bias.add_(0.1 * torch.randn(64, generator=g, device=DEV))
+    for shape in ((2, 5, 6, 64), (30, 64), (3, 11, 64)):
+        x = torch.randn(*shape, generator=g, device=DEV)
+        x = x.to(memory_format=torch.contiguous_format).requires_grad_()
+        dy = torch.randn(*shape, generator=g, device=DEV)
+        m.zero_grad()
+        y = m(x)
+        y.backward(dy)
+        x3 = x.detach().reshape(shape[0], -1, 64)
+        r = ref.groupnorm(x3, m.weight.detach(), m.bias.detach(), 4, 1e-5, True, dy.reshape(x3.shape))
+        for got, n in ((y.detach().view(x3.shape), "y"), (x.grad.view(x3.shape), "dx"), (m.weight.grad, "grad_w"),
+                       (m.bias.grad, "grad_b")):
+            assert ref.worst(got, r[n], r[n + "_tol"]) <= 1.0, n
+    # a channels-last view of [N, C, H, W], and an upstream gradient expanded from a scalar
+    img = torch.randn(2, 64, 5, 7, generator=g, device=DEV).to(memory_format=torch.channels_last).requires_grad_()
+    y = m(img.permute(0, 2, 3, 1))
+    y.sum().backward()
+    x3 = img.detach().permute(0, 2, 3, 1).reshape(2, 35, 64)
+    r = ref.groupnorm(x3, m.weight.detach(), m.bias.detach(), 4, 1e-5, True, torch.ones_like(x3))
+    assert ref.worst(img.grad.permute(0, 2, 3, 1).reshape(2, 35, 64), r["dx"], r["dx_tol"]) <= 1.0
+
+
+def test_training_step_captured(ag):
+    """Forward and backward of rotary, group norm and router through autograd
+    in one CUDA graph, replayed on new inputs (no eager graph of the same
+    leaves is alive during the capture)."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    m = ag.GroupNorm(4, 64, act="silu", device=DEV)
+    x = torch.randn(48, 4, 16, generator=g, device=DEV)
+    pos, f = torch.arange(48, device=DEV), torch.tensor([1.0, 0.1], device=DEV)
+
+    def step():
+        q, _ = ag.rotary(x, None, pos, f)
+        h = m(q.reshape(48, 64))
+        gates, _, _, loss = ag.topk_router(h, 4, None, True)
+        ((gates ** 2).sum() + loss + h.square().mean()).backward()
+
+    def eager():
+        m.weight.grad = m.bias.grad = None
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step()
+        torch.cuda.current_stream().wait_stream(s)
+        return m.weight.grad.clone(), m.bias.grad.clone()
+
+    for _ in range(2):
+        eager()
+    m.weight.grad = m.bias.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    gw, gb = m.weight.grad, m.bias.grad
+    x.copy_(torch.randn(48, 4, 16, generator=g, device=DEV))
+    graph.replay()
+    got = gw.clone(), gb.clone()
+    want = eager()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -1,0 +1,240 @@
+"""GPU tests of group norm with an activation, channels last, against a plain
+64-bit implementation: per-head rows (S = 1), feature maps of many sizes, odd
+channel counts and group widths, strides and shifted pointers, offsets and
+outliers, constant groups, accumulation, empty sizes, gradients against the
+formula and against differences, determinism, other streams, graphs."""
+import pytest
+import torch
+
+import blockref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DTS = [torch.float32, torch.float16, torch.bfloat16]
+EPS = 2.0 ** -17
+
+
+@pytest.fixture(scope="module")
+def wsf():
+    import __graft_entry__
+    __graft_entry__.build()
+    import backward_ws_fwd_gb300 as m
+    return m
+
+
+def _inputs(N, S, C, dtype, seed=0, mean=0.5):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def r(*shape):
+        return torch.randn(*shape, generator=g, device=DEV)
+
+    x = (r(N, S, C) * (1 + 0.3 * r(N, 1, C)) + mean * (1 + r(N, 1, C))).to(dtype)
+    return x, 1 + 0.1 * r(C), 0.1 * r(C), r(N, S, C).to(dtype)
+
+
+def _compare(out, r):
+    for name, got in out.items():
+        q = ref.worst(got, r[name], r[name + "_tol"])
+        assert q <= 1.0, (name, q)
+
+
+def _check(wsf, x, w, b, dy, G, act):
+    y, mean, rstd = wsf.groupnorm_fwd(x, w, b, G, EPS, act)
+    dx, gw, gb = wsf.groupnorm_bwd(x, w, b, mean, rstd, dy, G, act)
+    torch.cuda.synchronize()
+    r = ref.groupnorm(x, w, b, G, EPS, act == "silu", dy)
+    _compare(dict(y=y, mean=mean, rstd=rstd, dx=dx, grad_w=gw, grad_b=gb), r)
+    return y, mean, rstd, dx, gw, gb
+
+
+SHAPES = [  # N, S, C, G
+    (1, 1, 1, 1), (3, 1, 64, 8), (5, 1, 4096, 32), (700, 1, 512, 4), (37, 1, 2048, 8), (9, 1, 320, 5),
+    (2, 1, 16384, 64), (64, 1, 96, 12), (1, 2, 2, 2), (2, 9, 30, 5), (3, 49, 320, 32), (2, 1024, 320, 32),
+    (1, 4096, 128, 32), (4, 100, 200, 1), (2, 333, 64, 64), (1, 7, 8200, 8), (6, 17, 24, 3), (1, 5000, 40, 4),
+    (2, 257, 1280, 32), (1, 3, 16384, 1), (13, 64, 48, 16)]
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("N,S,C,G", SHAPES)
+def test_matches_64_bits(wsf, dtype, act, N, S, C, G):
+    x, w, b, dy = _inputs(N, S, C, dtype, N + S + C)
+    _check(wsf, x, w, b, dy, G, act)
+
+
+@pytest.mark.parametrize("dtype", DTS)
+def test_larger_maps_and_batches(wsf, dtype):
+    """Several tiles a sample, samples over many blocks, rows of heads over all
+    blocks several times."""
+    for N, S, C, G in ((3, 9216, 128, 32), (40, 1024, 96, 8), (5000, 1, 1024, 8), (1, 40000, 64, 16)):
+        x, w, b, dy = _inputs(N, S, C, dtype, S)
+        _check(wsf, x, w, b, dy, G, "silu")
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("N,S,C,G,pad,mis", [(3, 20, 64, 8, 8, 0), (3, 20, 64, 8, 3, 0), (2, 33, 64, 4, 0, 1),
+                                             (9, 1, 256, 2, 8, 0), (9, 1, 256, 2, 1, 0), (2, 300, 40, 4, 24, 2)])
+def test_strides_and_guards(wsf, dtype, N, S, C, G, pad, mis):
+    x0, w, b, dy0 = _inputs(N, S, C, dtype, 5)
+    ld, gap = C + pad, 2 * (C + pad)
+
+    def place(t, fill=None):
+        buf = torch.full((N * (S * ld + gap) + mis + 8,), 7.0, dtype=dtype, device=DEV)
+        v = buf[mis:].as_strided((N, S, C), (S * ld + gap, ld, 1), mis)
+        if fill is None:
+            v.copy_(t)
+        return buf, v
+
+    x, dy = place(x0)[1], place(dy0)[1]
+    yb, y = place(x0, 7.0)
+    db, dx = place(x0, 7.0)
+    _, mean, rstd = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu", y=y)
+    _, gw, gb = wsf.groupnorm_bwd(x, w, b, mean, rstd, dy, G, "silu", dx=dx)
+    r = ref.groupnorm(x0, w, b, G, EPS, True, dy0)
+    _compare(dict(y=y, mean=mean, rstd=rstd, dx=dx, grad_w=gw, grad_b=gb), r)
+    for buf, v in ((yb, y), (db, dx)):
+        v.fill_(7.0)
+        assert bool((buf == 7.0).all())
+    if S == 1:  # [N, C] is [N, 1, C]
+        y2, m2, _ = wsf.groupnorm_fwd(x0[:, 0], w, b, G, EPS, "silu")
+        assert y2.shape == (N, C) and ref.worst(y2, r["y"][:, 0], r["y_tol"][:, 0]) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("N,S,C,G", [(4, 1, 1024, 8), (2, 600, 64, 8), (1, 9000, 32, 4)])
+def test_offsets_outliers_and_constants(wsf, dtype, N, S, C, G):
+    """A mean a hundred times the spread, one value a thousand times it (at the
+    first place, about which sums are shifted, and elsewhere), constant groups."""
+    x, w, b, dy = _inputs(N, S, C, torch.float32, 6, mean=0.0)
+    off = (x + 100.0).to(dtype)
+    _check(wsf, off, w, b, dy.to(dtype), G, "silu")
+    for at in ((0, 0, 0), (0, S - 1, C - 1), (N - 1, S // 2, 5)):
+        spike = x.clone()
+        spike[at] = 1000.0
+        _check(wsf, spike.to(dtype), w, b, dy.to(dtype), G, None)
+    flat = x.clone()
+    flat[0, :, :C // G] = 3.25
+    _check(wsf, flat.to(dtype), w, b, dy.to(dtype), G, "silu")
+
+
+def test_special_values_stay_in_their_group(wsf):
+    for N, S, C, G in ((6, 1, 512, 4), (3, 50, 64, 8)):
+        x, w, b, dy = _inputs(N, S, C, torch.bfloat16, 7)
+        y0, m0, r0 = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu")
+        d0 = wsf.groupnorm_bwd(x, w, b, m0, r0, dy, G, "silu")[0]
+        for bad in (torch.nan, torch.inf):
+            z = x.clone()
+            z[1, 0, 3] = bad
+            y, m, r = wsf.groupnorm_fwd(z, w, b, G, EPS, "silu")
+            d = wsf.groupnorm_bwd(z, w, b, m, r, dy, G, "silu")[0]
+            hit = torch.zeros(N, S, C, dtype=torch.bool, device=DEV)
+            hit[1, :, :C // G] = True
+            assert torch.equal(y[~hit], y0[~hit]) and torch.equal(d[~hit], d0[~hit])
+            assert bool(torch.isnan(m[1, 0])) or bool(torch.isinf(m[1, 0]))
+            assert not bool(torch.isfinite(d[hit]).any())
+
+
+def test_large_activations(wsf):
+    """z far out on both sides: silu and its derivative go to z and 0, not NaN."""
+    for dtype in DTS:
+        x, _, _, dy = _inputs(4, 30, 64, dtype, 8)
+        w = torch.full((64,), 60.0, device=DEV)
+        b = torch.linspace(-200, 200, 64, device=DEV)
+        _check(wsf, x, w, b, dy, 4, "silu")
+
+
+def test_accumulate_and_empty(wsf):
+    for N, S, C, G in ((7, 1, 256, 2), (3, 40, 96, 8)):
+        x, w, b, dy = _inputs(N, S, C, torch.bfloat16, 9)
+        y, mean, rstd = wsf.groupnorm_fwd(x, w, b, G, EPS)
+        dx, gw, gb = wsf.groupnorm_bwd(x, w, b, mean, rstd, dy, G)
+        aw, ab = torch.full_like(gw, 2.0), torch.full_like(gb, -3.0)
+        wsf.groupnorm_bwd(x, w, b, mean, rstd, dy, G, grad_w=aw, grad_b=ab, accumulate=True)
+        assert torch.equal(aw, 2.0 + gw) and torch.equal(ab, -3.0 + gb)
+    w, b = torch.ones(64, device=DEV), torch.zeros(64, device=DEV)
+    for N, S in ((0, 5), (3, 0), (0, 0), (0, 1)):
+        x = torch.empty(N, S, 64, dtype=torch.float16, device=DEV)
+        y, mean, rstd = wsf.groupnorm_fwd(x, w, b, 8)
+        assert y.shape == x.shape and mean.shape == (N, 8)
+        assert bool((mean == 0).all()) and bool((rstd == 0).all())
+        gw, gb = torch.full((64,), 2.0, device=DEV), torch.full((64,), 3.0, device=DEV)
+        wsf.groupnorm_bwd(x, w, b, mean, rstd, x, 8, grad_w=gw, grad_b=gb, accumulate=True)
+        assert bool((gw == 2).all()) and bool((gb == 3).all())
+        wsf.groupnorm_bwd(x, w, b, mean, rstd, x, 8, grad_w=gw, grad_b=gb)
+        assert bool((gw == 0).all()) and bool((gb == 0).all())
+
+
+@pytest.mark.parametrize("N,S,C,G", [(3, 1, 64, 2), (2, 21, 24, 3)])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_gradients_match_differences(wsf, N, S, C, G, act):
+    """f = Σ y·u along random directions of x, w and b: central differences of
+    the 64-bit forward, step 1e-4 (error of the order of 1e-8)."""
+    x, w, b, u = _inputs(N, S, C, torch.float32, 10)
+    _, mean, rstd = wsf.groupnorm_fwd(x, w, b, G, EPS, act)
+    grads = wsf.groupnorm_bwd(x, w, b, mean, rstd, u, G, act)
+    g = torch.Generator(device=DEV).manual_seed(2)
+
+    def f(*a):
+        return (ref.groupnorm(a[0], a[1], a[2], G, EPS, act == "silu")["y"] * u.double()).sum()
+
+    args = [x.double(), w.double(), b.double()]
+    for i in range(3):
+        for _ in range(3):
+            d = torch.randn(args[i].shape, generator=g, device=DEV, dtype=torch.float64)
+            up, dn = list(args), list(args)
+            up[i], dn[i] = args[i] + 1e-4 * d, args[i] - 1e-4 * d
+            num = (f(*up) - f(*dn)) / 2e-4
+            got = grads[i].double() * d
+            assert abs(float(num - got.sum())) <= 3e-5 * float(got.abs().sum()), i
+
+
+def test_same_bits(wsf):
+    for N, S, C, G in ((3000, 1, 512, 4), (8, 2000, 64, 8)):
+        x, w, b, dy = _inputs(N, S, C, torch.bfloat16, 11)
+        a = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu")
+        d = wsf.groupnorm_bwd(x, w, b, a[1], a[2], dy, G, "silu")
+        for _ in range(3):
+            for p, q in zip(a, wsf.groupnorm_fwd(x, w, b, G, EPS, "silu")):
+                assert torch.equal(p, q)
+            for p, q in zip(d, wsf.groupnorm_bwd(x, w, b, a[1], a[2], dy, G, "silu")):
+                assert torch.equal(p, q)
+
+
+def test_large_offsets(wsf):
+    """Samples whose elements lie behind the 2^31st of their tensor."""
+    N, S, C, G, step = 3, 4, 64, 4, 1 << 30
+    buf = torch.zeros((N - 1) * step + S * C, dtype=torch.bfloat16, device=DEV)
+    x = buf.as_strided((N, S, C), (step, C, 1))
+    x0, w, b, dy = _inputs(N, S, C, torch.bfloat16, 12)
+    x.copy_(x0)
+    y, mean, rstd = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu")
+    want = wsf.groupnorm_fwd(x0, w, b, G, EPS, "silu")
+    assert torch.equal(y, want[0]) and torch.equal(mean, want[1])
+    d = wsf.groupnorm_bwd(x, w, b, mean, rstd, dy, G, "silu")
+    for p, q in zip(d, wsf.groupnorm_bwd(x0, w, b, mean, rstd, dy, G, "silu")):
+        assert torch.equal(p, q)
+
+
+def test_streams_and_graphs(wsf):
+    for N, S, C, G in ((200, 1, 512, 4), (4, 500, 64, 8)):
+        x, w, b, dy = _inputs(N, S, C, torch.bfloat16, 13)
+        want = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        out = [torch.empty_like(t) for t in want]
+        wsf.groupnorm_fwd(x, w, b, G, EPS, "silu", *out, stream=s)
+        s.synchronize()
+        for p, q in zip(out, want):
+            assert torch.equal(p, q)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu")
+            grads = wsf.groupnorm_bwd(x, w, b, got[1], got[2], dy, G, "silu")
+        x.copy_(_inputs(N, S, C, torch.bfloat16, 14)[0])
+        for _ in range(2):
+            graph.replay()
+        again = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu")
+        for p, q in zip(got, again):
+            assert torch.equal(p, q)
+        for p, q in zip(grads, wsf.groupnorm_bwd(x, w, b, again[1], again[2], dy, G, "silu")):
+            assert torch.equal(p, q)

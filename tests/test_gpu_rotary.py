@@ -1,0 +1,220 @@
+"""GPU tests of rotary positions against a plain 64-bit implementation: both
+pair layouts, whole and part heads, odd sizes and strides (packed, heads before
+tokens, shifted pointers), far and negative positions, in place, guard bands,
+backward as transpose and inverse, other streams, graphs."""
+import pytest
+import torch
+
+import blockref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DTS = [torch.float32, torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module")
+def wsf():
+    import __graft_entry__
+    __graft_entry__.build()
+    import backward_ws_fwd_gb300 as m
+    return m
+
+
+def _rand(shape, dtype, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(shape, generator=g, device=DEV).to(dtype)
+
+
+def _freq(R):
+    f = 10000.0 ** (-torch.arange(0, R, 2, dtype=torch.float64) / max(R, 1))
+    return f.float().to(DEV)
+
+
+def _check(wsf, q, k, pos, freq, scale=1.0, inter=False, th=None):
+    x = [q.clone(), None if k is None else k.clone()]
+    for fn, sign in ((wsf.rotary_fwd, 1.0), (wsf.rotary_bwd, -1.0)):
+        out = fn(q, k, pos, freq, scale, inter)
+        torch.cuda.synchronize()
+        for a, y in zip(x, out):
+            if a is None:
+                assert y is None
+                continue
+            assert y.dtype == a.dtype and y.shape == a.shape
+            if a.dim() == 3:
+                a, y = a[None], y[None]
+            want, tol = ref.rotary(a, pos, freq, scale, inter, sign, th)
+            assert ref.worst(y, want, tol) <= 1.0, (a.shape, a.dtype, inter, sign)
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("B,S,Hq,Hk,D,R", [
+    (1, 1, 1, 0, 2, 2), (1, 1, 8, 2, 64, 64), (2, 7, 3, 1, 128, 128), (3, 33, 5, 5, 80, 40),
+    (2, 17, 4, 2, 96, 24), (1, 130, 2, 1, 50, 30), (5, 3, 1, 1, 7, 6), (2, 9, 2, 2, 64, 0),
+    (1, 5, 64, 8, 256, 256), (1, 3, 1, 1, 1030, 1024), (1, 4, 0, 3, 32, 16), (4, 1021, 6, 2, 72, 72)])
+def test_matches_64_bits(wsf, dtype, inter, B, S, Hq, Hk, D, R):
+    q = _rand((B, S, Hq, D), dtype, 1)
+    k = _rand((B, S, Hk, D), dtype, 2) if Hk else None
+    pos = torch.randint(0, 9000, (B, S), device=DEV, dtype=torch.int32 if S % 2 else torch.int64)
+    _check(wsf, q, k, pos, _freq(R), 1.25 if inter else 1.0, inter)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_far_and_negative_positions(wsf, dtype):
+    """Angles of far positions keep their accuracy (compared with the exact
+    product: a 64-bit one is off by 1e-5 radians here)."""
+    pos = torch.tensor([[0, 1, -1, 131071, 1 << 20, -(1 << 20), (1 << 31) - 1, -(1 << 31), 123456789,
+                         1 << 33, -(1 << 34) + 5]], device=DEV)
+    q = _rand((1, pos.shape[1], 2, 64), dtype, 3)
+    f = _freq(64)
+    g = _freq(64)
+    g[3], g[5], g[9] = -g[3], 0.0, 1e-42  # negative, zero and subnormal frequencies
+    for freq, inter in ((f, False), (f * 7.5, True), (g, False)):
+        _check(wsf, q, None, pos, freq, inter=inter, th=ref.angles(pos, freq)[:, :, None])
+
+
+def test_frequencies_that_are_not_finite_give_nan(wsf):
+    q = _rand((1, 4, 1, 8), torch.float32, 4)
+    f = torch.tensor([1.0, torch.inf, torch.nan, 0.5], device=DEV)
+    y, _ = wsf.rotary_fwd(q, None, torch.arange(4, device=DEV), f)
+    bad = torch.tensor([False, True, True, False] * 2, device=DEV)
+    assert bool(torch.isnan(y[..., bad]).all()) and bool(torch.isfinite(y[..., ~bad]).all())
+
+
+def test_nan_and_inf_stay_in_their_pairs(wsf):
+    q = _rand((2, 3, 4, 64), torch.bfloat16, 5)
+    clean, _ = wsf.rotary_fwd(q, None, torch.arange(3, device=DEV), _freq(64))
+    p = q.clone()
+    p[1, 2, 3, 5], p[0, 1, 0, 40] = torch.nan, torch.inf
+    y, _ = wsf.rotary_fwd(p, None, torch.arange(3, device=DEV), _freq(64))
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[1, 2, 3, [5, 37]] = True
+    hit[0, 1, 0, [8, 40]] = True
+    assert torch.equal(y[~hit], clean[~hit]) and not bool(torch.isfinite(y[hit]).any())
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,R", [(64, 64), (80, 40), (36, 20)])
+def test_layouts_strides_and_guards(wsf, dtype, inter, D, R):
+    """Packed projections, heads before tokens, gaps, shifted pointers; what
+    is not written stays as it was."""
+    B, S, Hq, Hk = 2, 19, 4, 2
+    pos = torch.randint(0, 5000, (B, S), device=DEV)
+    f = _freq(R)
+    packed = _rand((B, S, Hq + 2 * Hk, D), dtype, 6)
+    _check(wsf, packed[:, :, :Hq], packed[:, :, Hq:Hq + Hk], pos, f, 1.0, inter)
+    heads = _rand((B, Hq + Hk, S, D), dtype, 7)
+    _check(wsf, heads[:, :Hq].transpose(1, 2), heads[:, Hq:].transpose(1, 2), pos, f, 1.0, inter)
+    gaps = _rand((B, S + 3, Hq, D + 5), dtype, 8)[:, 1:S + 1, :, 3:D + 3]
+    _check(wsf, gaps, gaps[:, :, 1:2], pos, f, 0.5, inter)
+    # outputs inside guard bands
+    want, _ = wsf.rotary_fwd(gaps, None, pos, f, 1.0, inter)
+    buf = torch.full((B, S + 2, Hq + 1, D + 4), 7.0, dtype=dtype, device=DEV)
+    out = buf[:, 1:-1, :Hq, 2:D + 2]
+    wsf.rotary_fwd(gaps, None, pos, f, 1.0, inter, q_out=out)
+    assert torch.equal(out, want)
+    keep = torch.ones_like(buf, dtype=torch.bool)
+    keep[:, 1:-1, :Hq, 2:D + 2] = False
+    assert bool((buf[keep] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("inter", [False, True])
+def test_in_place(wsf, dtype, inter):
+    """q and k of one packed buffer, rotated where they lie; v is left alone.
+    [T, H, D] rows, one position row for every batch, [1, S] positions."""
+    B, S, Hq, Hk, D, R = 3, 21, 6, 2, 64, 32
+    f = _freq(R)
+    pos = torch.arange(100, 100 + S, device=DEV)
+    packed = _rand((B, S, Hq + 2 * Hk, D), dtype, 9)
+    before = packed.clone()
+    q, k = packed[:, :, :Hq], packed[:, :, Hq:Hq + Hk]
+    wq, wk = wsf.rotary_fwd(q, k, pos, f, 1.5, inter)
+    wsf.rotary_fwd(q, k, pos[None], f, 1.5, inter, q_out=q, k_out=k)
+    assert torch.equal(q, wq) and torch.equal(k, wk)
+    assert torch.equal(packed[:, :, Hq + Hk:], before[:, :, Hq + Hk:])
+    one = before[1, :, :Hq]  # [T, H, D]
+    y, _ = wsf.rotary_fwd(one, None, pos, f, 1.5, inter)
+    assert torch.equal(y, wq[1])
+    # heads before tokens, batches interleaved with k's
+    heads = before.transpose(1, 2).contiguous()
+    q, k = heads[:, :Hq].transpose(1, 2), heads[:, Hq:Hq + Hk].transpose(1, 2)
+    wsf.rotary_fwd(q, k, pos, f, 1.5, inter, q_out=q, k_out=k)
+    assert torch.equal(q, wq) and torch.equal(k, wk)
+
+
+def test_backward_is_the_transpose_and_undoes_the_forward(wsf):
+    q = _rand((2, 50, 3, 96), torch.float32, 10)
+    dy = _rand((2, 50, 3, 96), torch.float32, 11)
+    pos = torch.randint(-4000, 4000, (2, 50), device=DEV)
+    for inter in (False, True):
+        y, _ = wsf.rotary_fwd(q, None, pos, _freq(64), 1.7, inter)
+        dq, _ = wsf.rotary_bwd(dy, None, pos, _freq(64), 1.7, inter)
+        a, b = (y.double() * dy).sum(), (q.double() * dq).sum()
+        # both sums of 28800 products, each good to 8·U of the pair's magnitudes
+        assert abs(a - b) <= 16 * ref.U * 1.7 * 2 * (q.abs().double() + 1).mul(dy.abs() + 1).sum()
+        back, _ = wsf.rotary_bwd(y, None, pos, _freq(64), 1.0 / 1.7, inter)
+        big = 2 * q.abs().amax()
+        assert float((back[..., :64] - q[..., :64]).abs().max()) <= 24 * ref.U * 1.7 * float(big)
+
+
+def test_refusals_leave_the_outputs(wsf):
+    q = _rand((1, 4, 2, 8), torch.float32, 12)
+    pos, f = torch.arange(4, device=DEV), _freq(8)
+    buf = q.clone()
+    with pytest.raises(wsf.WsfError) as e:  # shifted by one head
+        wsf.rotary_fwd(buf[:, :, :1], None, pos, f, q_out=buf[:, :, 0:1].as_strided((1, 4, 1, 8), (64, 16, 8, 1), 4))
+    assert e.value.status == wsf.ERR_OVERLAP
+    with pytest.raises(wsf.WsfError) as e:  # an expanded output
+        wsf.rotary_fwd(q, None, pos, f, q_out=torch.zeros(1, 4, 1, 8, device=DEV).expand(1, 4, 2, 8))
+    assert e.value.status == wsf.ERR_BAD_STRIDE
+    torch.cuda.synchronize()
+    assert torch.equal(buf, q)
+
+
+def test_expanded_input_empty_sizes(wsf):
+    x = _rand((1, 1, 1, 64), torch.bfloat16, 13).expand(2, 5, 3, 64)
+    _check(wsf, x, None, torch.arange(5, device=DEV), _freq(64))
+    for shape in ((0, 4, 2, 8), (2, 0, 2, 8), (2, 4, 0, 8)):
+        y, _ = wsf.rotary_fwd(torch.empty(shape, device=DEV), None,
+                              torch.zeros(shape[:2], device=DEV, dtype=torch.int64), _freq(8))
+        assert y.shape == shape
+
+
+def test_large_offsets(wsf):
+    """Elements behind the 2^31st: a long packed cache, its last tokens."""
+    S, H, D = 70000, 2, 16
+    step = 32768  # elements a token
+    buf = torch.zeros(S * step, dtype=torch.float16, device=DEV)
+    view = buf.as_strided((1, S, H, D), (S * step, step, D, 1))
+    view.copy_(_rand((1, S, H, D), torch.float16, 14))
+    assert (S - 1) * step > 1 << 31
+    pos = torch.arange(S, device=DEV)
+    y, _ = wsf.rotary_fwd(view, None, pos, _freq(D))
+    want, tol = ref.rotary(view, pos, _freq(D), 1.0, False)
+    assert ref.worst(y, want, tol) <= 1.0
+    wsf.rotary_fwd(view, None, pos, _freq(D), q_out=view)
+    assert torch.equal(view, y)
+
+
+def test_streams_and_graphs(wsf):
+    q = _rand((4, 64, 8, 128), torch.bfloat16, 15)
+    k = _rand((4, 64, 2, 128), torch.bfloat16, 16)
+    pos, f = torch.randint(0, 9000, (4, 64), device=DEV), _freq(128)
+    want = wsf.rotary_fwd(q, k, pos, f)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = (torch.empty_like(q), torch.empty_like(k))
+    wsf.rotary_fwd(q, k, pos, f, q_out=out[0], k_out=out[1], stream=s)
+    s.synchronize()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = wsf.rotary_fwd(q, k, pos, f)
+    pos += 17
+    q.mul_(-1)
+    g.replay()
+    again = wsf.rotary_fwd(q, k, pos, f)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])

@@ -1,0 +1,236 @@
+"""GPU tests of the top-k router and its balance loss against a plain 64-bit
+implementation: every number of lanes a row, ties, masked experts and rows,
+NaN, odd widths and strides, k from 1 to 32, normalised and plain gates,
+gradients against the formula and against differences, accumulated counts,
+determinism, other streams, graphs."""
+import pytest
+import torch
+
+import blockref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DTS = [torch.float32, torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module")
+def wsf():
+    import __graft_entry__
+    __graft_entry__.build()
+    import backward_ws_fwd_gb300 as m
+    return m
+
+
+def _logits(T, E, dtype, seed, scale=1.5):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(T, E, generator=g, device=DEV) * scale +
+            0.5 * torch.randn(E, generator=g, device=DEV)).to(dtype)
+
+
+def _check(wsf, l, k, mask=None, renorm=False, seed=0):
+    T, E = l.shape
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    dg = torch.randn(T, k, generator=g, device=DEV)
+    dl = torch.tensor(0.7, device=DEV)
+    gates, ids, counts, loss = wsf.router_fwd(l, k, mask, renorm)
+    dlog = wsf.router_bwd(l, ids, counts, dg, dl, renorm)
+    torch.cuda.synchronize()
+    r = ref.router(l, k, mask, renorm, dg, 0.7)
+    assert torch.equal(ids.long(), r["ids"]) and torch.equal(counts.long(), r["counts"])
+    assert ref.worst(gates, r["gates"], r["gates_tol"]) <= 1.0
+    assert abs(float(loss) - r["loss"]) <= r["loss_tol"], (float(loss), r["loss"])
+    assert ref.worst(dlog, r["dlogits"], r["dlogits_tol"]) <= 1.0
+    return gates, ids, counts, loss, dlog
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("T,E,k", [
+    (1, 1, 1), (3, 2, 2), (33, 5, 3), (100, 8, 8), (65, 9, 2), (500, 16, 4), (129, 30, 6),
+    (1000, 60, 4), (77, 64, 8), (2000, 72, 1), (513, 128, 8), (31, 129, 10), (300, 200, 32),
+    (700, 256, 8), (40, 257, 8), (90, 384, 6), (55, 512, 10), (20, 513, 3), (17, 1000, 32), (9, 1024, 8)])
+def test_matches_64_bits(wsf, dtype, T, E, k):
+    l = _logits(T, E, dtype, T + E)
+    for renorm in (False, True):
+        _check(wsf, l, k, None, renorm)
+    mask = torch.rand(T, device=DEV) > 0.3
+    _check(wsf, l, k, mask, E % 2 == 0)
+
+
+@pytest.mark.parametrize("dtype", DTS)
+def test_ties_go_to_the_lowest_index(wsf, dtype):
+    for E, k in ((8, 8), (60, 8), (256, 8), (300, 12)):
+        _check(wsf, torch.zeros(50, E, dtype=dtype, device=DEV), k)
+        g = torch.Generator(device=DEV).manual_seed(E)
+        few = torch.randint(0, 3, (200, E), generator=g, device=DEV).to(dtype)
+        signed = torch.where(torch.rand(200, E, generator=g, device=DEV) < 0.5, few, -few)  # −0 and +0
+        _check(wsf, few, k)
+        _check(wsf, signed, k, renorm=True)
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("E,k", [(7, 3), (64, 8), (256, 6), (520, 8)])
+def test_masked_experts_and_rows(wsf, dtype, E, k):
+    """−inf logits have gate 0 and no gradient; a row of them alone does not
+    count; neither does a row that the mask leaves out, whatever it holds."""
+    T = 67
+    l = _logits(T, E, dtype, 3)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    l[torch.rand(T, E, generator=g, device=DEV) < 0.7] = -torch.inf  # rows with fewer than k left
+    l[5] = -torch.inf
+    l[T - 1] = -torch.inf
+    for renorm in (False, True):
+        gates, ids, _, loss, dl = _check(wsf, l, k, None, renorm)
+        assert bool((ids[5] == -1).all()) and bool((gates[5] == 0).all()) and bool((dl[5] == 0).all())
+        assert bool((dl[l == -torch.inf] == 0).all())
+    mask = torch.ones(T, dtype=torch.bool, device=DEV)
+    mask[10], mask[66] = False, False
+    clean = wsf.router_fwd(l, k, mask)
+    dirty = l.clone()
+    dirty[10, 0], dirty[10, 1] = torch.nan, torch.inf
+    got = wsf.router_fwd(dirty, k, mask)
+    for a, b in zip(clean, got):
+        assert torch.equal(a, b)
+    dg = torch.randn(T, k, device=DEV)
+    dl = wsf.router_bwd(dirty, got[1], got[2], dg, torch.ones((), device=DEV))
+    assert bool((dl[10] == 0).all()) and bool(torch.isfinite(dl).all())
+    lowest = torch.where(l == -torch.inf, torch.full_like(l, torch.finfo(dtype).min), l)
+    _check(wsf, lowest, k)  # a mask of the type's lowest value is a value
+
+
+@pytest.mark.parametrize("dtype", DTS)
+def test_no_row_counts(wsf, dtype):
+    l = _logits(40, 64, dtype, 5)
+    for l2, mask in ((l, torch.zeros(40, dtype=torch.bool, device=DEV)), (torch.full_like(l, -torch.inf), None),
+                     (l[:0], None)):
+        gates, ids, counts, loss = wsf.router_fwd(l2, 4, mask)
+        assert bool((gates == 0).all()) and bool((ids == -1).all()) and bool((counts == 0).all())
+        assert float(loss) == 0.0
+        dl = wsf.router_bwd(l2, ids, counts, torch.ones(l2.shape[0], 4, device=DEV), torch.ones((), device=DEV))
+        assert bool((dl == 0).all())
+
+
+@pytest.mark.parametrize("dtype", DTS)
+def test_nan_and_inf_rows_keep_valid_ids(wsf, dtype):
+    l = _logits(30, 60, dtype, 6)
+    l[3, 7], l[4], l[9, 2], l[11, 50] = torch.nan, torch.nan, -torch.nan, torch.inf
+    gates, ids, counts, loss = wsf.router_fwd(l, 6)
+    for t in (3, 4, 9, 11):
+        assert bool(torch.isnan(gates[t]).all())
+    assert bool(torch.isnan(loss)) and int(counts.sum()) == 30 * 6
+    assert bool(((ids >= 0) & (ids < 60)).all())
+    assert all(len(set(r)) == 6 for r in ids.tolist())
+    rest = [t for t in range(30) if t not in (3, 4, 9, 11)]
+    r = ref.router(l[rest], 6)
+    assert torch.equal(ids[rest].long(), r["ids"]) and ref.worst(gates[rest], r["gates"], r["gates_tol"]) <= 1.0
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("E,pad,mis", [(64, 8, 0), (64, 0, 1), (64, 3, 0), (60, 4, 0), (256, 1, 3)])
+def test_strides_and_guards(wsf, dtype, E, pad, mis):
+    T, k, ld = 45, 5, E + pad
+    src = _logits(T, E, dtype, 7)
+    buf = torch.full((T * ld + mis + 8,), 3.0, dtype=dtype, device=DEV)
+    l = buf[mis:mis + T * ld].view(T, ld)[:, :E]
+    l.copy_(src)
+    want = _check(wsf, src, k)
+    got = wsf.router_fwd(l, k)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    out = torch.full((T * ld + mis + 8,), 7.0, dtype=dtype, device=DEV)
+    dl = out[mis:mis + T * ld].view(T, ld)[:, :E]
+    g = torch.Generator(device=DEV).manual_seed(0)
+    wsf.router_bwd(l, got[1], got[2], torch.randn(T, k, generator=g, device=DEV), torch.tensor(0.7, device=DEV),
+                   dlogits=dl)
+    assert torch.equal(dl, want[4])
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[mis:mis + T * ld].view(T, ld)[:, :E] = False
+    assert bool((out[keep] == 7.0).all())
+
+
+def test_large_spread(wsf):
+    """Logits hundreds apart: probabilities down to 0, no overflow."""
+    for dtype in DTS:
+        for scale in (30.0, 200.0):
+            _check(wsf, _logits(100, 128, dtype, 8, scale), 8, renorm=True)
+            _check(wsf, _logits(100, 40, dtype, 8, scale), 3)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradient_matches_differences(wsf, renorm):
+    """f = Σ gates·u + c·loss with the choice held: central differences of the
+    64-bit forward along random directions, step 1e-4 (their own error, third
+    derivatives of a softmax times 1e-8, stays below 1e-6)."""
+    T, E, k = 12, 24, 4
+    l = _logits(T, E, torch.float32, 9)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    u = torch.randn(T, k, generator=g, device=DEV)
+    gates, ids, counts, loss = wsf.router_fwd(l, k, None, renorm)
+    dl = wsf.router_bwd(l, ids, counts, u, torch.tensor(2.5, device=DEV), renorm)
+
+    def f(x):
+        p = torch.softmax(x, 1)
+        q = p.gather(1, ids.long())
+        q = q / q.sum(1, keepdim=True) if renorm else q
+        return (q * u.double()).sum() + 2.5 * E * (counts.double() / (k * T) * p.sum(0) / T).sum()
+
+    for i in range(6):
+        d = torch.randn(T, E, generator=g, device=DEV, dtype=torch.float64)
+        num = (f(l.double() + 1e-4 * d) - f(l.double() - 1e-4 * d)) / 2e-4
+        assert abs(float(num - (dl.double() * d).sum())) <= 2e-5 * float((dl.double() * d).abs().sum())
+
+
+def test_parts_of_the_gradient_and_common_counts(wsf):
+    """dgates or dloss missing is zero; counts of two micro-batches give the
+    gradient of their common loss."""
+    l = _logits(64, 32, torch.float32, 10)
+    gates, ids, counts, loss = wsf.router_fwd(l, 3)
+    dg, one = torch.randn(64, 3, device=DEV), torch.ones((), device=DEV)
+    zero = torch.zeros((), device=DEV)
+    assert torch.equal(wsf.router_bwd(l, ids, counts, dg, None), wsf.router_bwd(l, ids, counts, dg, zero))
+    for renorm in (False, True):
+        assert torch.equal(wsf.router_bwd(l, ids, counts, None, one, renorm),
+                           wsf.router_bwd(l, ids, counts, torch.zeros_like(dg), one, renorm))
+    both = wsf.router_fwd(l, 3)
+    a, b = wsf.router_fwd(l[:40], 3), wsf.router_fwd(l[40:], 3)
+    c = a[2] + b[2]
+    assert torch.equal(c, both[2])
+    whole = wsf.router_bwd(l, ids, c, dg, one)
+    parts = torch.cat([wsf.router_bwd(l[:40], a[1], c, dg[:40], one), wsf.router_bwd(l[40:], b[1], c, dg[40:], one)])
+    assert torch.equal(whole, parts)
+
+
+def test_many_rows_same_bits(wsf):
+    """All blocks busy, rows a block several turns; two runs, the same bits."""
+    l = _logits(70001, 64, torch.bfloat16, 11)
+    a = _check(wsf, l, 6, torch.rand(70001, device=DEV) > 0.1, True)
+    l2 = _logits(30000, 256, torch.bfloat16, 12)
+    b = wsf.router_fwd(l2, 8)
+    for _ in range(3):
+        for x, y in zip(b, wsf.router_fwd(l2, 8)):
+            assert torch.equal(x, y)
+    _check(wsf, l2, 8)
+    assert int(a[2].sum()) > 0
+
+
+def test_streams_and_graphs(wsf):
+    l = _logits(900, 64, torch.bfloat16, 13)
+    want = wsf.router_fwd(l, 4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = [torch.empty_like(t) for t in want]
+    wsf.router_fwd(l, 4, None, False, *out, stream=s)
+    s.synchronize()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+    one = torch.ones((), device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = wsf.router_fwd(l, 4)
+        dl = wsf.router_bwd(l, got[1], got[2], got[0], one)
+    l.copy_(_logits(900, 64, torch.bfloat16, 14))
+    for _ in range(2):
+        graph.replay()
+    again = wsf.router_fwd(l, 4)
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
+    assert torch.equal(dl, wsf.router_bwd(l, again[1], again[2], again[0], one))
