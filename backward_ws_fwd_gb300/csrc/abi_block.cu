@@ -199,12 +199,11 @@ bool clash(const Span* outs, int no, const Span* ins, int ni) {
     return false;
 }
 
-bool groupnorm_sizes(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
+bool groupnorm_sizes(int64_t N, int64_t S, int64_t C, int64_t G) {
     if (N < 0 || S < 0 || C < 0 || G < 1 || C > wsf::kGroupNormMaxC || C % G) return false;
-    // grids and workspaces stay inside int32 launches and int64 bytes
+    // sizes and workspaces in bytes stay inside int64
     if (C == 0 || N == 0 || S == 0) return N <= INT32_MAX;
-    if (N > INT32_MAX || S > (INT64_MAX / 64) / C / N) return false;
-    return wsf::groupnorm_units(N, S, C, G, dtype) <= INT32_MAX && N * G <= INT32_MAX;
+    return N <= INT32_MAX / G && S <= (INT64_MAX / 4096) / C / N;
 }
 
 Tensor rows_of(const void* p, int64_t n, int64_t s, int64_t N, int64_t S, int64_t C, int es) {
@@ -289,7 +288,7 @@ int router_bwd(const void* logits, int64_t ld, const int* ids, const int* counts
 }
 
 size_t groupnorm_fwd_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
-    if (!valid_dtype(dtype) || !groupnorm_sizes(N, S, C, G, dtype)) return SIZE_MAX;
+    if (!valid_dtype(dtype) || !groupnorm_sizes(N, S, C, G)) return SIZE_MAX;
     return (size_t)wsf::groupnorm_fwd_floats(N, S, C, G, dtype) * 4;
 }
 
@@ -298,7 +297,7 @@ int groupnorm_fwd(const void* x, int64_t x_n, int64_t x_s, const float* w, const
                   void* workspace, size_t workspace_bytes, int64_t N, int64_t S, int64_t C,
                   int64_t G, int dtype, wsf_stream_t stream) {
     if (!valid_dtype(dtype)) return WSF_ERR_BAD_DTYPE;
-    if (!groupnorm_sizes(N, S, C, G, dtype)) return WSF_ERR_BAD_SHAPE;
+    if (!groupnorm_sizes(N, S, C, G)) return WSF_ERR_BAD_SHAPE;
     if (!(eps >= 0.0f && eps <= 3.0e38f) || (act != WSF_ACT_NONE && act != WSF_ACT_SILU))
         return WSF_ERR_BAD_ARG;
     const int es = elt_bytes(dtype);
@@ -330,7 +329,7 @@ int groupnorm_fwd(const void* x, int64_t x_n, int64_t x_s, const float* w, const
 }
 
 size_t groupnorm_bwd_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
-    if (!valid_dtype(dtype) || !groupnorm_sizes(N, S, C, G, dtype)) return SIZE_MAX;
+    if (!valid_dtype(dtype) || !groupnorm_sizes(N, S, C, G)) return SIZE_MAX;
     return (size_t)wsf::groupnorm_bwd_floats(N, S, C, G, dtype) * 4;
 }
 
@@ -340,7 +339,7 @@ int groupnorm_bwd(const void* x, int64_t x_n, int64_t x_s, const float* w, const
                   float* grad_b, int accumulate, void* workspace, size_t workspace_bytes,
                   int64_t N, int64_t S, int64_t C, int64_t G, int dtype, wsf_stream_t stream) {
     if (!valid_dtype(dtype)) return WSF_ERR_BAD_DTYPE;
-    if (!groupnorm_sizes(N, S, C, G, dtype)) return WSF_ERR_BAD_SHAPE;
+    if (!groupnorm_sizes(N, S, C, G)) return WSF_ERR_BAD_SHAPE;
     if ((accumulate != 0 && accumulate != 1) || (act != WSF_ACT_NONE && act != WSF_ACT_SILU))
         return WSF_ERR_BAD_ARG;
     const int es = elt_bytes(dtype);

@@ -71,8 +71,6 @@ struct GroupNormBwd {
 };
 int64_t groupnorm_fwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dtype);
 int64_t groupnorm_bwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dtype);
-// Row tiles of all samples (the launches' grid).
-int64_t groupnorm_units(int64_t N, int64_t S, int64_t C, int64_t G, int dtype);
 cudaError_t launch_groupnorm_fwd(const GroupNormFwd& a, cudaStream_t s);
 cudaError_t launch_groupnorm_bwd(const GroupNormBwd& a, cudaStream_t s);
 
