@@ -28,57 +28,211 @@ namespace wsf {
 namespace {
 
 constexpr int NT = 256;
+constexpr int kFwdStages = 8, kBwdStages = 6;  // of Walk
 
-// V consecutive elements as they are loaded (16 bytes, or one element), and as
-// binary32.
+// V consecutive values as binary32, arithmetic two lanes an instruction
+// (packed f32x2) where V > 1.
+template <int V>
+struct Vals {
+    uint64_t p[V / 2];
+    __device__ __forceinline__ static Vals splat(float a) {
+        Vals r;
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) r.p[i] = f2_pack(a, a);
+        return r;
+    }
+    __device__ __forceinline__ static Vals of(const float (&f)[V]) {
+        Vals r;
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) r.p[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+        return r;
+    }
+    __device__ __forceinline__ void to(float (&f)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) f2_unpack(p[i], f[2 * i], f[2 * i + 1]);
+    }
+};
+template <>
+struct Vals<1> {
+    float f;
+    __device__ __forceinline__ static Vals splat(float a) { return Vals{a}; }
+    __device__ __forceinline__ static Vals of(const float (&g)[1]) { return Vals{g[0]}; }
+    __device__ __forceinline__ void to(float (&g)[1]) const { g[0] = f; }
+};
+#define GN_VALS_OP(NAME, PAIR, ONE)                                                     \
+    template <int V>                                                                    \
+    __device__ __forceinline__ Vals<V> NAME(const Vals<V>& a, const Vals<V>& b) {       \
+        Vals<V> r;                                                                      \
+        if constexpr (V == 1) {                                                         \
+            r.f = ONE(a.f, b.f);                                                        \
+        } else {                                                                        \
+            _Pragma("unroll") for (int i = 0; i < V / 2; i++) r.p[i] = PAIR(a.p[i], b.p[i]); \
+        }                                                                               \
+        return r;                                                                       \
+    }
+GN_VALS_OP(add, f2_add, __fadd_rn)
+GN_VALS_OP(sub, f2_sub, __fsub_rn)
+GN_VALS_OP(mul, f2_mul, __fmul_rn)
+#undef GN_VALS_OP
+template <int V>
+__device__ __forceinline__ Vals<V> fma(const Vals<V>& a, const Vals<V>& b, const Vals<V>& c) {
+    Vals<V> r;
+    if constexpr (V == 1) {
+        r.f = fmaf(a.f, b.f, c.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) r.p[i] = f2_fma(a.p[i], b.p[i], c.p[i]);
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ float total(const Vals<V>& a) {
+    if constexpr (V == 1) {
+        return a.f;
+    } else {
+        uint64_t t = a.p[0];
+#pragma unroll
+        for (int i = 1; i < V / 2; i++) t = f2_add(t, a.p[i]);
+        float x, y;
+        f2_unpack(t, x, y);
+        return x + y;
+    }
+}
+
+// V consecutive elements as they are loaded (16 bytes, or one element).
 template <typename T, int V>
 struct Held {
     Raw16 raw;
     __device__ __forceinline__ void load(const T* p) { raw = ld_keep(p); }
-    __device__ __forceinline__ void widen(float (&f)[V]) const { Elt<T>::widen(raw, f); }
+    __device__ __forceinline__ Vals<V> widen() const {
+        float f[V];
+        Elt<T>::widen(raw, f);
+        return Vals<V>::of(f);
+    }
 };
 template <typename T>
 struct Held<T, 1> {
     float raw;
     __device__ __forceinline__ void load(const T* p) { raw = Elt<T>::load1(p); }
-    __device__ __forceinline__ void widen(float (&f)[1]) const { f[0] = raw; }
+    __device__ __forceinline__ Vals<1> widen() const { return Vals<1>{raw}; }
 };
 template <typename T, int V>
-__device__ __forceinline__ void store_v(T* p, const float (&f)[V]) {
+__device__ __forceinline__ void store_v(T* p, const Vals<V>& v) {
+    float f[V];
+    v.to(f);
     if constexpr (V == 1)
         Elt<T>::store1(p, f[0]);
     else
         st_stream(p, Elt<T>::narrow(f));
 }
 
+// The K tensors' 16-byte vectors that one thread walks, staged S - 1 steps
+// ahead in shared memory with cp.async: a thread copies and reads only its own
+// slots, so no thread waits for another and the loads in flight do not take
+// registers.  The walk is unrolled S times (GN_WALK), which makes every slot's
+// address a constant offset.  For V == 1 (unaligned) plain loads.
+template <typename T, int V, int K, int S>
+struct Walk {
+    static constexpr int stages = S;
+    static constexpr size_t bytes = V == 1 ? 0 : (size_t)S * K * NT * 16;
+    const T* p[K];
+    int64_t step[K];
+    bool use[K];  // a tensor that is not used reads as zeros
+    int left;     // steps not yet asked for
+    Raw16* ring;
+
+    __device__ __forceinline__ void ask(int slot) {
+        if (left > 0) {
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                if (use[k]) cp_async16(ring + (slot * K + k) * NT, p[k], 16);
+                p[k] += step[k];
+            }
+        }
+        left--;
+        cp_async_commit();
+    }
+    // Count steps from p on; each is waited for by its next().
+    __device__ __forceinline__ void start(void* smem, int count) {
+        left = count;
+        if constexpr (V > 1) {
+            ring = reinterpret_cast<Raw16*>(smem) + threadIdx.x;
+#pragma unroll
+            for (int k = 0; k < K; k++)
+                if (!use[k])
+                    for (int i = 0; i < S; i++) ring[(i * K + k) * NT] = raw_zero();
+#pragma unroll
+            for (int i = 0; i < S - 1; i++) ask(i);
+        }
+    }
+    // Step j, i = j mod S.
+    __device__ __forceinline__ void next(int i, Held<T, V> (&h)[K]) {
+        if constexpr (V > 1) {
+            ask((i + S - 1) % S);
+            cp_async_wait<S - 1>();
+#pragma unroll
+            for (int k = 0; k < K; k++) h[k].raw = ring[(i * K + k) * NT];
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                h[k].load(p[k]);
+                p[k] += step[k];
+            }
+        }
+    }
+};
+#define GN_WALK(walk, i, count)                                \
+    for (int gn_j = 0; gn_j < (count); gn_j += walk.stages)    \
+        _Pragma("unroll") for (int i = 0; i < walk.stages; i++) \
+            if (gn_j + i < (count))
+
 // sigmoid(z): for binary32 storage by expf and a true division, for 16-bit
-// storage by the hardware's exponential and reciprocal (a few 2⁻²², far
-// below the 2⁻¹¹ half step of the outputs).
-template <typename T>
-__device__ __forceinline__ float sigmoid(float z) {
-    if constexpr (sizeof(T) == 4)
-        return 1.0f / (1.0f + expf(-z));
+// storage by the hardware's exponential and reciprocal (together a few 2⁻²²,
+// far below the 2⁻¹¹ half step of the outputs).
+template <typename T, int V>
+__device__ __forceinline__ Vals<V> sigmoid(const Vals<V>& z) {
+    float f[V];
+    if constexpr (sizeof(T) == 4) {
+        z.to(f);
+#pragma unroll
+        for (int i = 0; i < V; i++) f[i] = 1.0f / (1.0f + expf(-f[i]));
+    } else {
+        mul(z, Vals<V>::splat(-1.4426950408889634f)).to(f);
+#pragma unroll
+        for (int i = 0; i < V; i++) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f[i]));
+        add(Vals<V>::of(f), Vals<V>::splat(1.0f)).to(f);
+#pragma unroll
+        for (int i = 0; i < V; i++) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f[i]));
+    }
+    return Vals<V>::of(f);
+}
+template <typename T, bool Silu, int V>
+__device__ __forceinline__ Vals<V> activate(const Vals<V>& z) {
+    if constexpr (!Silu)
+        return z;
     else
-        return __fdividef(1.0f, 1.0f + __expf(-z));
+        return mul(z, sigmoid<T, V>(z));
 }
-template <typename T, bool Silu>
-__device__ __forceinline__ float activate(float z) {
-    if constexpr (!Silu) return z;
-    return z * sigmoid<T>(z);
-}
-// dy·silu′(z)
-template <typename T, bool Silu>
-__device__ __forceinline__ float through(float dy, float z) {
-    if constexpr (!Silu) return dy;
-    const float q = sigmoid<T>(z);
-    return dy * q * fmaf(z, 1.0f - q, 1.0f);
+// dy·silu′(z), silu′ = q·(1 + z·(1 − q)) with q the sigmoid
+template <typename T, bool Silu, int V>
+__device__ __forceinline__ Vals<V> through(const Vals<V>& dy, const Vals<V>& z) {
+    if constexpr (!Silu) {
+        return dy;
+    } else {
+        const Vals<V> one = Vals<V>::splat(1.0f), q = sigmoid<T, V>(z);
+        return mul(mul(dy, q), fma(z, sub(one, q), one));
+    }
 }
 
 struct Shape {
     int64_t N, S, xn, xs, yn, ys, gn, gs;  // strides of x, of y or dx, of dy
     int C, G, Cg;
     int tiles;     // row tiles of a sample
+    int joins;     // partial statistics of a sample that the second pass joins,
+    int64_t jrows; // each of jrows rows (the last: what is left)
+    int lg;        // lanes that join a group's sums (a power of two)
     int64_t rows;  // rows of a tile
+    int64_t xstep, ystep, gstep;  // strides of the rows that a thread walks
 };
 
 // Threads of a block over a tile: cv vectors a row, RL rows at a time.
@@ -94,9 +248,10 @@ struct Lanes {
 
 // A unit is a tile of a sample.
 struct Unit {
-    int64_t n, tile, s0;
+    int n, tile;
+    int64_t s0;
     int rows;
-    __device__ __forceinline__ Unit(const Shape& d, int64_t u) {
+    __device__ __forceinline__ Unit(const Shape& d, int u) {
         n = u / d.tiles;
         tile = u - n * d.tiles;
         s0 = tile * d.rows;
@@ -111,18 +266,54 @@ struct Rows {
     __device__ __forceinline__ int of(int r) const { return base + (r < extra); }
 };
 
-// Groups of V consecutive channels from ch on, without a division a channel.
-template <int V>
-__device__ __forceinline__ void groups_of(int ch, int Cg, int (&g)[V]) {
-    g[0] = ch / Cg;
-    int left = (g[0] + 1) * Cg - ch;
-#pragma unroll
-    for (int i = 1; i < V; i++) {
-        left--;
-        const bool next = left == 0;
-        g[i] = g[i - 1] + next;
-        left = next ? Cg : left;
+// Threads that share a channel once a tile's sums are in shared memory: Q
+// parts, part q taking the row lanes q, q + Q, ...
+struct Parts {
+    int Q, q;
+    __device__ __forceinline__ Parts(int C, int RL) {
+        Q = C < NT ? min(NT / C, RL) : 1;
+        q = C < NT ? (int)threadIdx.x / C : 0;
     }
+};
+
+// Sum over a group's lg lanes, which are neighbours.
+__device__ __forceinline__ float lanes_sum(float v, int lg) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lg) v += __shfl_xor_sync(FULL_MASK, v, o);
+    return v;
+}
+
+// The same for two values at once, unrolled.
+__device__ __forceinline__ void lanes_sum2(float& a, float& b, int lg) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o < lg) {
+            const float p = __shfl_xor_sync(FULL_MASK, a, o), q = __shfl_xor_sync(FULL_MASK, b, o);
+            a += p;
+            b += q;
+        }
+    }
+}
+
+// Per-channel values of a vector of channels, from per-group ones.
+template <int V, typename F>
+__device__ __forceinline__ Vals<V> by_group(int ch, int Cg, F value) {
+    float f[V];
+    int g = ch / Cg, left = (g + 1) * Cg - ch;
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+        f[i] = value(g);
+        if (--left == 0) g++, left = Cg;
+    }
+    return Vals<V>::of(f);
+}
+template <int V>
+__device__ __forceinline__ Vals<V> params(const float* p, int ch) {
+    float f[V];
+#pragma unroll
+    for (int i = 0; i < V; i++) f[i] = __ldg(p + ch + i);
+    return Vals<V>::of(f);
 }
 
 // ---------------------------------------------------------------------------
@@ -133,179 +324,200 @@ __device__ __forceinline__ void groups_of(int ch, int Cg, int (&g)[V]) {
 // First pass: mean and squared deviations of every group over a tile.  A
 // thread sums about its first value; threads' means and deviations are joined
 // about their common mean, first the row lanes of a channel (Q threads a
-// channel where there are few), then a group's channels by a warp.
+// channel where there are few), then a group's channels by lg lanes.
 template <typename T, int V>
 __global__ void __launch_bounds__(NT, 4) gn_stats_kernel(const T* x, const Shape d, float2* part) {
-    constexpr int U = V == 1 ? 8 : 4;
+    constexpr int S = kFwdStages;
     extern __shared__ float4 smem[];
+    __shared__ float part_rows[NT];              // rows of a part
     const Lanes t(d.C, V);
-    float* sm = reinterpret_cast<float*>(smem);  // [RL][C] means
+    // [RL][C] means, behind the staging
+    float* sm = reinterpret_cast<float*>(smem) + Walk<T, V, 1, S>::bytes / 4;
     float* sq = sm + (size_t)t.RL * d.C;         // [RL][C] squared deviations
-    pdl_wait();
     const Unit un(d, blockIdx.x);
     const Rows rows(un.rows, t.RL);
+    const Parts pt(d.C, t.RL);
+    if (threadIdx.x < pt.Q) {
+        int n = 0;
+        for (int r = threadIdx.x; r < t.RL; r += pt.Q) n += rows.of(r);
+        part_rows[threadIdx.x] = (float)n;
+    }
+    pdl_wait();
     const T* base = x + un.n * d.xn + un.s0 * d.xs;
     if (t.r < t.RL) {
         const int cnt = rows.of(t.r);
         const float inv = cnt ? 1.0f / cnt : 0.f;
-        const int64_t step = t.RL * d.xs;
         for (int c = t.c; c < t.cv; c += NT) {
-            float k[V], a[V], b[V];
-#pragma unroll
-            for (int i = 0; i < V; i++) k[i] = a[i] = b[i] = 0.f;
-            const T* p = base + (int64_t)t.r * d.xs + c * V;
+            Vals<V> k = Vals<V>::splat(0.f), a = k, b = k;
+            Walk<T, V, 1, S> in;
+            in.p[0] = base + (int64_t)t.r * d.xs + c * V;
+            in.step[0] = d.xstep;
+            in.use[0] = true;
+            Held<T, V> first;
             if (cnt) {
-                Held<T, V> h;
-                h.load(p);
-                h.widen(k);
+                first.load(in.p[0]);
+                k = first.widen();
             }
-            for (int j = 1; j < cnt; j += U) {
-                Held<T, V> h[U];
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    if (j + u < cnt) p += step;
-                    h[u].load(p);
-                }
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    if (j + u < cnt) {
-                        float f[V];
-                        h[u].widen(f);
-#pragma unroll
-                        for (int i = 0; i < V; i++) {
-                            const float q = f[i] - k[i];
-                            a[i] += q;
-                            b[i] = fmaf(q, q, b[i]);
-                        }
-                    }
-                }
+            in.start(smem, cnt);
+            GN_WALK(in, i, cnt) {
+                Held<T, V> h[1];
+                in.next(i, h);
+                const Vals<V> q = sub(h[0].widen(), k);
+                a = add(a, q);
+                b = fma(q, q, b);
             }
+            float m[V], e[V];
+            const Vals<V> mean = mul(a, Vals<V>::splat(inv));
+            add(k, mean).to(m);
+            sub(b, mul(mean, a)).to(e);
 #pragma unroll
             for (int i = 0; i < V; i++) {
-                const float m = a[i] * inv;
-                sm[t.r * d.C + c * V + i] = k[i] + m;
-                sq[t.r * d.C + c * V + i] = fmaxf(fmaf(-m, a[i], b[i]), 0.f);
+                sm[t.r * d.C + c * V + i] = m[i];
+                sq[t.r * d.C + c * V + i] = fmaxf(e[i], 0.f);
             }
         }
     }
     __syncthreads();
-    // row lanes part, part + Q, ... of a channel, into lane `part`
-    const int Q = d.C < NT ? min(NT / d.C, t.RL) : 1;
-    const int part0 = d.C < NT ? (int)threadIdx.x / d.C : 0;
-    if (t.RL > 1 && part0 < Q) {
-        for (int c = d.C < NT ? (int)threadIdx.x % d.C : (int)threadIdx.x; c < d.C; c += NT) {
+    if (t.RL > 1 && pt.q < pt.Q) {  // into row lane q
+        const float n = part_rows[pt.q], inv = n > 0.f ? 1.0f / n : 0.f;
+        for (int c = d.C < NT ? (int)threadIdx.x - pt.q * d.C : (int)threadIdx.x; c < d.C; c += NT) {
             float s = 0.f;
-            int n = 0;
-            for (int r = part0; r < t.RL; r += Q) {
-                s = fmaf((float)rows.of(r), sm[r * d.C + c], s);
-                n += rows.of(r);
-            }
-            const float m = n ? s / n : 0.f;
+            for (int r = pt.q; r < t.RL; r += pt.Q) s = fmaf((float)rows.of(r), sm[r * d.C + c], s);
+            const float m = s * inv;
             s = 0.f;
-            for (int r = part0; r < t.RL; r += Q) {
+            for (int r = pt.q; r < t.RL; r += pt.Q) {
                 const float e = sm[r * d.C + c] - m;
                 s += fmaf((float)rows.of(r) * e, e, sq[r * d.C + c]);
             }
-            sm[part0 * d.C + c] = m;
-            sq[part0 * d.C + c] = s;
+            sm[pt.q * d.C + c] = m;
+            sq[pt.q * d.C + c] = s;
         }
     }
     __syncthreads();
-    const int lane = threadIdx.x & 31;
+    const int j0 = threadIdx.x & (d.lg - 1);
     const float inv = 1.0f / ((float)un.rows * d.Cg);
-    for (int g = threadIdx.x >> 5; g < d.G; g += NT / 32) {
-        float s = 0.f, mean = 0.f;
-#pragma unroll
-        for (int pass = 0; pass < 2; pass++) {
-            s = 0.f;
-            for (int q = 0; q < Q; q++) {
-                int n = 0;  // rows of the part
-                for (int r = q; r < t.RL; r += Q) n += rows.of(r);
-                for (int c = lane; c < d.Cg; c += 32) {
-                    const int at = q * d.C + g * d.Cg + c;
-                    const float e = sm[at] - mean;
-                    s += pass ? fmaf((float)n * e, e, sq[at]) : (float)n * e;
+    for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
+        const int g = g0 + threadIdx.x / d.lg;
+        const bool on = g < d.G;
+        float s = 0.f;
+        if (on)
+            for (int q = 0; q < pt.Q; q++)
+                for (int c = j0; c < d.Cg; c += d.lg)
+                    s = fmaf(part_rows[q], sm[q * d.C + g * d.Cg + c], s);
+        const float m = lanes_sum(s, d.lg) * inv;
+        s = 0.f;
+        if (on)
+            for (int q = 0; q < pt.Q; q++)
+                for (int c = j0; c < d.Cg; c += d.lg) {
+                    const float e = sm[q * d.C + g * d.Cg + c] - m;
+                    s += fmaf(part_rows[q] * e, e, sq[q * d.C + g * d.Cg + c]);
                 }
-            }
-            s = group_sum<32>(s);
-            if (pass == 0) mean = s * inv;
-        }
-        if (lane == 0) part[(int64_t)blockIdx.x * d.G + g] = make_float2(mean, s);
+        s = lanes_sum(s, d.lg);
+        if (on && j0 == 0) part[(int64_t)blockIdx.x * d.G + g] = make_float2(m, s);
     }
     pdl_trigger();
 }
 
-// Second pass.  The block first joins its sample's tiles, a warp a group; the
-// first tile's block writes the statistics out.
+// Where a sample has many tiles, their statistics (or the backward's sums) are
+// joined by a warp a (sample, group) before the second pass.
+constexpr int kJoin = 48;  // partials that the second pass joins itself
+
+template <bool Sums>
+__global__ void __launch_bounds__(NT) gn_join_kernel(const float2* part, float2* out,
+                                                     const Shape d) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t u = (int64_t)blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
+    if (u < d.N * d.G) {
+        const float2* p = part + u / d.G * d.tiles * d.G + u % d.G;
+        const float whole = (float)d.rows, last = (float)(d.S - (d.tiles - 1) * d.rows);
+        float s = 0.f, q = 0.f;
+#pragma unroll 8
+        for (int i = lane; i < d.tiles; i += 32) {
+            const float2 v = p[(int64_t)i * d.G];
+            s = fmaf(Sums ? 1.f : i + 1 < d.tiles ? whole : last, v.x, s);
+            if (Sums) q += v.y;
+        }
+        s = group_sum<32>(s);
+        if (!Sums) {
+            s /= (float)d.S;
+#pragma unroll 8
+            for (int i = lane; i < d.tiles; i += 32) {
+                const float2 v = p[(int64_t)i * d.G];
+                const float e = v.x - s;
+                q += fmaf((i + 1 < d.tiles ? whole : last) * d.Cg * e, e, v.y);
+            }
+        }
+        q = group_sum<32>(q);
+        if (lane == 0) out[u] = make_float2(s, q);
+    }
+    pdl_trigger();
+}
+
+// Second pass.  The block first joins its sample's partial statistics, lg
+// lanes a group; the first tile's block writes the statistics out.
 template <typename T, int V, bool Silu>
-__global__ void __launch_bounds__(NT, 4) gn_apply_kernel(const T* x, T* y, const float* w,
+__global__ void __launch_bounds__(NT, 3) gn_apply_kernel(const T* x, T* y, const float* w,
                                                       const float* b, float eps, float* mean,
                                                       float* rstd, const float2* part,
                                                       const Shape d) {
-    constexpr int U = V == 1 ? 8 : 4;
     extern __shared__ float4 smem[];
-    float2* st = reinterpret_cast<float2*>(smem);  // [G] mean, 1/deviation
+    Walk<T, V, 1, kFwdStages> in;
+    float2* st = reinterpret_cast<float2*>(smem) + in.bytes / 8;  // [G] μ, r
     const Lanes t(d.C, V);
+    const Unit un(d, (int)gridDim.x - 1 - (int)blockIdx.x);
+    const int cnt = t.r < t.RL && t.c < t.cv ? Rows(un.rows, t.RL).of(t.r) : 0;
+    auto begin = [&](int c) {
+        in.p[0] = x + un.n * d.xn + (un.s0 + t.r) * d.xs + c * V;
+        in.step[0] = d.xstep;
+        in.use[0] = true;
+        in.start(smem, cnt);
+    };
     pdl_wait();
-    const Unit un(d, (int64_t)gridDim.x - 1 - blockIdx.x);
-    {
-        const int lane = threadIdx.x & 31;
-        for (int g = threadIdx.x >> 5; g < d.G; g += NT / 32) {
-            const float2* p = part + un.n * d.tiles * d.G + g;
-            float s = 0.f;
-            for (int i = lane; i < d.tiles; i += 32)
-                s = fmaf((float)min(d.rows, d.S - i * d.rows), p[(int64_t)i * d.G].x, s);
-            const float m = group_sum<32>(s) / (float)d.S;
-            s = 0.f;
-            for (int i = lane; i < d.tiles; i += 32) {
+    begin(t.c);  // in flight while the tiles are joined
+    const int j0 = threadIdx.x & (d.lg - 1);
+    for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
+        const int g = g0 + threadIdx.x / d.lg;
+        const bool on = g < d.G;
+        const float2* p = part + (int64_t)un.n * d.joins * d.G + g;
+        const float whole = (float)d.jrows, last = (float)(d.S - (d.joins - 1) * d.jrows);
+        float s = 0.f;
+        if (on) {
+#pragma unroll 4
+            for (int i = j0; i < d.joins; i += d.lg)
+                s = fmaf(i + 1 < d.joins ? whole : last, p[(int64_t)i * d.G].x, s);
+        }
+        const float m = lanes_sum(s, d.lg) / (float)d.S;
+        s = 0.f;
+        if (on) {
+#pragma unroll 4
+            for (int i = j0; i < d.joins; i += d.lg) {
                 const float2 q = p[(int64_t)i * d.G];
                 const float e = q.x - m;
-                s += fmaf((float)min(d.rows, d.S - i * d.rows) * d.Cg * e, e, q.y);
+                s += fmaf((i + 1 < d.joins ? whole : last) * d.Cg * e, e, q.y);
             }
-            s = group_sum<32>(s);
-            if (lane == 0) {
-                const float r = 1.0f / sqrtf(s / ((float)d.S * d.Cg) + eps);
-                st[g] = make_float2(m, r);
-                if (un.tile == 0) mean[un.n * d.G + g] = m, rstd[un.n * d.G + g] = r;
-            }
+        }
+        s = lanes_sum(s, d.lg);
+        if (on && j0 == 0) {
+            const float r = 1.0f / sqrtf(s / ((float)d.S * d.Cg) + eps);
+            st[g] = make_float2(m, r);
+            if (un.tile == 0) mean[(int64_t)un.n * d.G + g] = m, rstd[(int64_t)un.n * d.G + g] = r;
         }
     }
     __syncthreads();
     if (t.r < t.RL) {
-        const int64_t xstep = t.RL * d.xs, ystep = t.RL * d.ys;
-        const int cnt = Rows(un.rows, t.RL).of(t.r);
         for (int c = t.c; c < t.cv; c += NT) {
-            float mu[V], rw[V], sh[V];
-            int g[V];
-            groups_of<V>(c * V, d.Cg, g);
-#pragma unroll
-            for (int i = 0; i < V; i++) {
-                const float2 q = st[g[i]];
-                mu[i] = q.x;
-                rw[i] = q.y * __ldg(w + c * V + i);
-                sh[i] = __ldg(b + c * V + i);
-            }
-            const T* p = x + un.n * d.xn + (un.s0 + t.r) * d.xs + c * V;
+            if (c != t.c) begin(c);
+            const Vals<V> mu = by_group<V>(c * V, d.Cg, [&](int g) { return st[g].x; });
+            const Vals<V> rw = mul(by_group<V>(c * V, d.Cg, [&](int g) { return st[g].y; }),
+                                   params<V>(w, c * V));
+            const Vals<V> sh = params<V>(b, c * V);
             T* o = y + un.n * d.yn + (un.s0 + t.r) * d.ys + c * V;
-            for (int j = 0; j < cnt; j += U) {
-                Held<T, V> h[U];
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    h[u].load(p);
-                    if (j + u < cnt - 1) p += xstep;
-                }
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    if (j + u < cnt) {
-                        float f[V];
-                        h[u].widen(f);
-#pragma unroll
-                        for (int i = 0; i < V; i++)
-                            f[i] = activate<T, Silu>(fmaf(f[i] - mu[i], rw[i], sh[i]));
-                        store_v<T, V>(o, f);
-                        o += ystep;
-                    }
-                }
+            GN_WALK(in, i, cnt) {
+                Held<T, V> h[1];
+                in.next(i, h);
+                store_v<T, V>(o, activate<T, Silu, V>(fma(sub(h[0].widen(), mu), rw, sh)));
+                o += d.ystep;
             }
         }
     }
@@ -314,84 +526,72 @@ __global__ void __launch_bounds__(NT, 4) gn_apply_kernel(const T* x, T* y, const
 
 // ---------------------------------------------------------------------------
 // Backward, first pass: a block walks units u0 .. u1 and writes each unit's
-// groups' sums (m₂, m₁ shares) and, over all of them, the channels' sums.
+// groups' sums (shares of M·m₂ and M·m₁) and, over all of them, the channels'.
 template <typename T, int V, bool Silu>
 __global__ void __launch_bounds__(NT, 3) gn_bwd_sums_kernel(const T* x, const T* dy, const float* w,
                                                          const float* b, const float* mean,
                                                          const float* rstd, const Shape d,
                                                          float2* part_g, float* part_a,
                                                          float* part_b) {
-    constexpr int U = 2;
     extern __shared__ float4 smem[];
     const Lanes t(d.C, V);
-    float* sa = reinterpret_cast<float*>(smem);  // [RL][C]
+    // [RL][C], behind the staging
+    float* sa = reinterpret_cast<float*>(smem) + Walk<T, V, 2, kBwdStages>::bytes / 4;
     float* sb = sa + (size_t)t.RL * d.C;         // [RL][C]
     float* ta = part_a + (int64_t)blockIdx.x * d.C;  // [C] the block's own row
     float* tb = part_b + (int64_t)blockIdx.x * d.C;
-    pdl_wait();
     const int64_t units = d.N * d.tiles;
-    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-    const int Q = d.C < NT ? min(NT / d.C, t.RL) : 1;
-    const int part0 = d.C < NT ? (int)threadIdx.x / d.C : 0;
-    for (int64_t u = u0; u < u1; u++) {
+    const int u0 = (int)(units * blockIdx.x / gridDim.x);
+    const int u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    const Parts pt(d.C, t.RL);
+    pdl_wait();
+    for (int u = u0; u < u1; u++) {
         const Unit un(d, u);
         if (t.r < t.RL) {
-            const int64_t xstep = t.RL * d.xs, gstep = t.RL * d.gs;
             const int cnt = Rows(un.rows, t.RL).of(t.r);
+            const float *mn = mean + (int64_t)un.n * d.G, *rn = rstd + (int64_t)un.n * d.G;
             for (int c = t.c; c < t.cv; c += NT) {
-                float mu[V], rw[V], bc[V], A[V], B[V];
-                int g[V];
-                groups_of<V>(c * V, d.Cg, g);
+                const int64_t s0 = un.s0 + t.r;
+                Walk<T, V, 2, kBwdStages> in;
+                in.p[0] = x + un.n * d.xn + s0 * d.xs + c * V;
+                in.p[1] = dy + un.n * d.gn + s0 * d.gs + c * V;
+                in.step[0] = d.xstep;
+                in.step[1] = d.gstep;
+                in.use[0] = in.use[1] = true;
+                in.start(smem, cnt);
+                const Vals<V> mu = by_group<V>(c * V, d.Cg, [&](int g) { return __ldg(mn + g); });
+                const Vals<V> rw = mul(by_group<V>(c * V, d.Cg, [&](int g) { return __ldg(rn + g); }),
+                                       params<V>(w, c * V));
+                const Vals<V> bc = params<V>(b, c * V);
+                Vals<V> A = Vals<V>::splat(0.f), B = A;
+                GN_WALK(in, i, cnt) {
+                    Held<T, V> h[2];
+                    in.next(i, h);
+                    const Vals<V> f = sub(h[0].widen(), mu);
+                    const Vals<V> dz = through<T, Silu, V>(h[1].widen(), fma(f, rw, bc));
+                    A = fma(dz, f, A);  // times r below
+                    B = add(B, dz);
+                }
+                float fa[V], fb[V];
+                mul(A, by_group<V>(c * V, d.Cg, [&](int g) { return __ldg(rn + g); })).to(fa);
+                B.to(fb);
 #pragma unroll
                 for (int i = 0; i < V; i++) {
-                    mu[i] = mean[un.n * d.G + g[i]];
-                    rw[i] = rstd[un.n * d.G + g[i]] * __ldg(w + c * V + i);
-                    bc[i] = __ldg(b + c * V + i);
-                    A[i] = B[i] = 0.f;
-                }
-                const T* p = x + un.n * d.xn + (un.s0 + t.r) * d.xs + c * V;
-                const T* q = dy + un.n * d.gn + (un.s0 + t.r) * d.gs + c * V;
-                for (int j = 0; j < cnt; j += U) {
-                    Held<T, V> hx[U], hg[U];
-#pragma unroll
-                    for (int k = 0; k < U; k++) {
-                        hx[k].load(p);
-                        hg[k].load(q);
-                        if (j + k < cnt - 1) p += xstep, q += gstep;
-                    }
-#pragma unroll
-                    for (int k = 0; k < U; k++) {
-                        if (j + k < cnt) {
-                            float f[V], h[V];
-                            hx[k].widen(f);
-                            hg[k].widen(h);
-#pragma unroll
-                            for (int i = 0; i < V; i++) {
-                                f[i] -= mu[i];
-                                const float dz = through<T, Silu>(h[i], fmaf(f[i], rw[i], bc[i]));
-                                A[i] = fmaf(dz, f[i], A[i]);  // times r below
-                                B[i] += dz;
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < V; i++) {
-                    sa[t.r * d.C + c * V + i] = A[i] * rstd[un.n * d.G + g[i]];
-                    sb[t.r * d.C + c * V + i] = B[i];
+                    sa[t.r * d.C + c * V + i] = fa[i];
+                    sb[t.r * d.C + c * V + i] = fb[i];
                 }
             }
         }
         __syncthreads();
-        if (t.RL > 1 && Q > 1 && part0 < Q) {  // row lanes of a channel, Q threads a channel
-            const int c = (int)threadIdx.x % d.C;
+        if (pt.Q > 1 && pt.q < pt.Q) {  // into row lane q
+            const int c = (int)threadIdx.x - pt.q * d.C;
             float A = 0.f, B = 0.f;
-            for (int r = part0; r < t.RL; r += Q) A += sa[r * d.C + c], B += sb[r * d.C + c];
-            sa[part0 * d.C + c] = A;
-            sb[part0 * d.C + c] = B;
+            for (int r = pt.q; r < t.RL; r += pt.Q) A += sa[r * d.C + c], B += sb[r * d.C + c];
+            sa[pt.q * d.C + c] = A;
+            sb[pt.q * d.C + c] = B;
         }
         __syncthreads();
-        const int left = Q > 1 ? Q : t.RL;
+        const int left = pt.Q > 1 ? pt.Q : t.RL;
         for (int c = threadIdx.x; c < d.C; c += NT) {
             float A = sa[c], B = sb[c];
             for (int r = 1; r < left; r++) A += sa[r * d.C + c], B += sb[r * d.C + c];
@@ -401,94 +601,84 @@ __global__ void __launch_bounds__(NT, 3) gn_bwd_sums_kernel(const T* x, const T*
             sb[c] = B * __ldg(w + c);
         }
         __syncthreads();
-        const int lane = threadIdx.x & 31;
-        for (int g = threadIdx.x >> 5; g < d.G; g += NT / 32) {
+        const int j0 = threadIdx.x & (d.lg - 1);
+        for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
+            const int g = g0 + threadIdx.x / d.lg;
             float A = 0.f, B = 0.f;
-            for (int c = lane; c < d.Cg; c += 32) A += sa[g * d.Cg + c], B += sb[g * d.Cg + c];
-            A = group_sum<32>(A);
-            B = group_sum<32>(B);
-            if (lane == 0) part_g[u * d.G + g] = make_float2(A, B);
+            if (g < d.G)
+                for (int c = j0; c < d.Cg; c += d.lg) A += sa[g * d.Cg + c], B += sb[g * d.Cg + c];
+            A = lanes_sum(A, d.lg);
+            B = lanes_sum(B, d.lg);
+            if (g < d.G && j0 == 0) part_g[(int64_t)u * d.G + g] = make_float2(A, B);
         }
         __syncthreads();
     }
     pdl_trigger();
 }
 
+// dx = dz·(w·r) − (x − μ)·(r²·m₂) − r·m₁
 template <typename T, int V, bool Silu>
 __global__ void __launch_bounds__(NT, 3) gn_bwd_apply_kernel(const T* x, const T* dy, T* dx,
                                                           const float* w, const float* b,
                                                           const float* mean, const float* rstd,
                                                           const float2* part, const Shape d) {
-    constexpr int U = 2;
     extern __shared__ float4 smem[];
-    float4* st = smem;  // [G] μ, r, r·m₁, r²·m₂
+    Walk<T, V, 2, kBwdStages> in;
+    float4* st = smem + in.bytes / 16;  // [G] μ, r, −r·m₁, −r²·m₂
     const Lanes t(d.C, V);
+    const Unit un(d, (int)gridDim.x - 1 - (int)blockIdx.x);
+    const int cnt = t.r < t.RL && t.c < t.cv ? Rows(un.rows, t.RL).of(t.r) : 0;
+    auto begin = [&](int c) {
+        const int64_t s0 = un.s0 + t.r;
+        in.p[0] = x + un.n * d.xn + s0 * d.xs + c * V;
+        in.p[1] = dy + un.n * d.gn + s0 * d.gs + c * V;
+        in.step[0] = d.xstep;
+        in.step[1] = d.gstep;
+        in.use[0] = in.use[1] = true;
+        in.start(smem, cnt);
+    };
     pdl_wait();
-    const Unit un(d, (int64_t)gridDim.x - 1 - blockIdx.x);
-    {
-        const int lane = threadIdx.x & 31;
-        const float inv = 1.0f / ((float)d.S * d.Cg);
-        for (int g = threadIdx.x >> 5; g < d.G; g += NT / 32) {
-            const float2* p = part + un.n * d.tiles * d.G + g;
-            float A = 0.f, B = 0.f;
-            for (int i = lane; i < d.tiles; i += 32) {
+    begin(t.c);  // in flight while the tiles are joined
+    const int j0 = threadIdx.x & (d.lg - 1);
+    const float inv = 1.0f / ((float)d.S * d.Cg);
+    for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
+        const int g = g0 + threadIdx.x / d.lg;
+        const bool on = g < d.G;
+        const float2* p = part + (int64_t)un.n * d.joins * d.G + g;
+        float A = 0.f, B = 0.f;
+        if (on) {
+#pragma unroll 4
+            for (int i = j0; i < d.joins; i += d.lg) {
                 const float2 q = p[(int64_t)i * d.G];
                 A += q.x;
                 B += q.y;
             }
-            A = group_sum<32>(A);
-            B = group_sum<32>(B);
-            if (lane == 0) {
-                const float r = rstd[un.n * d.G + g];
-                st[g] = make_float4(mean[un.n * d.G + g], r, r * (B * inv), r * r * (A * inv));
-            }
+        }
+        A = lanes_sum(A, d.lg);
+        B = lanes_sum(B, d.lg);
+        if (on && j0 == 0) {
+            const float r = rstd[(int64_t)un.n * d.G + g];
+            st[g] = make_float4(mean[(int64_t)un.n * d.G + g], r, -r * (B * inv), -r * r * (A * inv));
         }
     }
     __syncthreads();
     if (t.r < t.RL) {
-        const int64_t xstep = t.RL * d.xs, gstep = t.RL * d.gs, ystep = t.RL * d.ys;
-        const int cnt = Rows(un.rows, t.RL).of(t.r);
         for (int c = t.c; c < t.cv; c += NT) {
-            // dx = dz·(w·r) − (x − μ)·(r²·m₂) − r·m₁
-            float mu[V], rw[V], bc[V], e2[V], e1[V];
-            int g[V];
-            groups_of<V>(c * V, d.Cg, g);
-#pragma unroll
-            for (int i = 0; i < V; i++) {
-                const float4 q = st[g[i]];
-                mu[i] = q.x;
-                rw[i] = q.y * __ldg(w + c * V + i);
-                bc[i] = __ldg(b + c * V + i);
-                e1[i] = q.z;
-                e2[i] = q.w;
-            }
-            const T* p = x + un.n * d.xn + (un.s0 + t.r) * d.xs + c * V;
-            const T* q = dy + un.n * d.gn + (un.s0 + t.r) * d.gs + c * V;
+            if (c != t.c) begin(c);
+            const Vals<V> mu = by_group<V>(c * V, d.Cg, [&](int g) { return st[g].x; });
+            const Vals<V> rw = mul(by_group<V>(c * V, d.Cg, [&](int g) { return st[g].y; }),
+                                   params<V>(w, c * V));
+            const Vals<V> e1 = by_group<V>(c * V, d.Cg, [&](int g) { return st[g].z; });
+            const Vals<V> e2 = by_group<V>(c * V, d.Cg, [&](int g) { return st[g].w; });
+            const Vals<V> bc = params<V>(b, c * V);
             T* o = dx + un.n * d.yn + (un.s0 + t.r) * d.ys + c * V;
-            for (int j = 0; j < cnt; j += U) {
-                Held<T, V> hx[U], hg[U];
-#pragma unroll
-                for (int k = 0; k < U; k++) {
-                    hx[k].load(p);
-                    hg[k].load(q);
-                    if (j + k < cnt - 1) p += xstep, q += gstep;
-                }
-#pragma unroll
-                for (int k = 0; k < U; k++) {
-                    if (j + k < cnt) {
-                        float f[V], h[V];
-                        hx[k].widen(f);
-                        hg[k].widen(h);
-#pragma unroll
-                        for (int i = 0; i < V; i++) {
-                            f[i] -= mu[i];
-                            const float dz = through<T, Silu>(h[i], fmaf(f[i], rw[i], bc[i]));
-                            f[i] = fmaf(dz, rw[i], -fmaf(f[i], e2[i], e1[i]));
-                        }
-                        store_v<T, V>(o, f);
-                        o += ystep;
-                    }
-                }
+            GN_WALK(in, i, cnt) {
+                Held<T, V> h[2];
+                in.next(i, h);
+                const Vals<V> f = sub(h[0].widen(), mu);
+                const Vals<V> dz = through<T, Silu, V>(h[1].widen(), fma(f, rw, bc));
+                store_v<T, V>(o, fma(dz, rw, fma(f, e2, e1)));
+                o += d.ystep;
             }
         }
     }
@@ -508,8 +698,15 @@ __global__ void __launch_bounds__(1024) gn_grad_kernel(const float* part_a, cons
     const float* part = blockIdx.y ? part_b : part_a;
     float* out = blockIdx.y ? gb : gw;
     Acc2 a = acc2_zero();
-    if (c < C)
-        for (int64_t p = stripe; p < P; p += 32) acc2_add1(a, part[p * C + c]);
+    if (c < C) {
+        for (int64_t p = stripe; p < P; p += 32 * 8) {
+            float v[8];  // eight loads in flight
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = p + 32 * i < P ? part[(p + 32 * i) * C + c] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; i++) acc2_add1(a, v[i]);
+        }
+    }
     st[stripe][col] = make_float2(a.hi, a.lo);
     __syncthreads();
     for (int h = 16; h > 0; h >>= 1) {
@@ -532,8 +729,8 @@ __global__ void __launch_bounds__(1024) gn_grad_kernel(const float* part_a, cons
 // CPL 16-byte vectors a lane, so both statistics, and the backward's two
 // group sums, are butterflies over those lanes and every value is read once.
 // A warp keeps its place in the row (w, b and the gradient sums stay in
-// registers) and walks the samples, U of them in flight.
-constexpr int RT = 256, RW = RT / 32;
+// registers) and walks the samples.
+constexpr int RT = NT, RW = RT / 32;
 
 struct RowShape {
     int64_t N, xn, yn, gn;
@@ -541,6 +738,7 @@ struct RowShape {
     int lpg, cpg;   // lanes of a group (a power of two), vectors of a group
     int spr, rpw;   // lanes of a row, rows of a warp (1 if a row fills it)
     int segs, RB;   // grid: warps that a row spreads over, blocks along the samples
+    int64_t step, xstep, ystep, gstep;  // samples of a turn of the grid, and their strides
 };
 
 // A lane's place: its group, its vectors' first element, its row of the warp.
@@ -558,166 +756,166 @@ struct Place {
     }
 };
 
-__device__ __forceinline__ float lanes_sum(float v, int lpg) {
-    for (int o = lpg >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
-    return v;
-}
-
 template <typename T, int CPL, bool Silu>
-__global__ void __launch_bounds__(RT, CPL == 1 ? 3 : 2)
+__global__ void __launch_bounds__(RT, CPL == 1 ? 4 : 2)
     gn_rows_fwd_kernel(const T* x, T* y, const float* w, const float* b, float eps, float* mean,
                        float* rstd, const RowShape d) {
-    constexpr int V = Elt<T>::V, U = CPL == 1 ? 4 : 2;
+    constexpr int V = Elt<T>::V;
+    extern __shared__ float4 smem[];
     const Place t(d, V);
     const float inv = 1.0f / (float)d.Cg;
     bool has[CPL];
-    float wc[CPL][V], bc[CPL][V];
+    Vals<V> wc[CPL], bc[CPL];
     pdl_wait();
 #pragma unroll
     for (int c = 0; c < CPL; c++) {
         has[c] = t.on && t.j + c * d.lpg < d.cpg;
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-            wc[c][i] = has[c] ? __ldg(w + t.at + c * d.lpg * V + i) : 0.f;
-            bc[c][i] = has[c] ? __ldg(b + t.at + c * d.lpg * V + i) : 0.f;
+        wc[c] = bc[c] = Vals<V>::splat(0.f);
+        if (has[c]) {
+            wc[c] = params<V>(w, t.at + c * d.lpg * V);
+            bc[c] = params<V>(b, t.at + c * d.lpg * V);
         }
     }
-    const int64_t step = (int64_t)d.RB * RW * d.rpw;
-    const int64_t first = ((int64_t)(blockIdx.x / d.segs) * RW + (threadIdx.x >> 5)) * d.rpw;
-    for (int64_t n0 = first; n0 < d.N; n0 += U * step) {
-        Raw16 raw[U][CPL];
+    int64_t n = ((int64_t)(blockIdx.x / d.segs) * RW + (threadIdx.x >> 5)) * d.rpw;
+    const int turns = n < d.N ? (int)((d.N - 1 - n) / d.step) + 1 : 0;  // of the warp
+    n += t.sub;
+    const int mine = n < d.N ? (int)((d.N - 1 - n) / d.step) + 1 : 0;   // of the lane
+    Walk<T, V, CPL, kFwdStages> in;
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int64_t n = n0 + u * step + t.sub;
+    for (int c = 0; c < CPL; c++) {
+        in.p[c] = x + n * d.xn + (has[c] ? t.at + c * d.lpg * V : 0);
+        in.step[c] = d.xstep;
+        in.use[c] = has[c];
+    }
+    in.start(smem, mine);
+    T* o = y + n * d.yn + t.at;
+    GN_WALK(in, i, turns) {
+        const int turn = gn_j + i;
+        Held<T, V> h[CPL];
+        in.next(i, h);
+        Vals<V> f[CPL], q = Vals<V>::splat(0.f);
 #pragma unroll
-            for (int c = 0; c < CPL; c++)
-                raw[u][c] = has[c] && n < d.N ? ld_stream(x + n * d.xn + t.at + c * d.lpg * V)
-                                              : raw_zero();
+        for (int c = 0; c < CPL; c++) {
+            if (d.rpw > 1 && turn >= mine) h[c].raw = raw_zero();
+            f[c] = h[c].widen();
+            q = add(q, f[c]);
         }
+        const float m = lanes_sum(total(q), d.lpg) * inv;
+        q = Vals<V>::splat(0.f);
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (n0 + u * step >= d.N) break;
-            const int64_t n = n0 + u * step + t.sub;
-            float f[CPL][V], s = 0.f;
-#pragma unroll
-            for (int c = 0; c < CPL; c++) {
-                Elt<T>::widen(raw[u][c], f[c]);
-#pragma unroll
-                for (int i = 0; i < V; i++) s += f[c][i];
-            }
-            const float m = lanes_sum(s, d.lpg) * inv;
-            s = 0.f;
-#pragma unroll
-            for (int c = 0; c < CPL; c++)
-#pragma unroll
-                for (int i = 0; i < V; i++) {
-                    f[c][i] -= m;
-                    if (has[c]) s = fmaf(f[c][i], f[c][i], s);
-                }
-            const float r = 1.0f / sqrtf(fmaf(lanes_sum(s, d.lpg), inv, eps));
-            if (n >= d.N) continue;
+        for (int c = 0; c < CPL; c++) {
+            f[c] = sub(f[c], Vals<V>::splat(has[c] ? m : 0.f));
+            q = fma(f[c], f[c], q);
+        }
+        const float r = 1.0f / sqrtf(fmaf(lanes_sum(total(q), d.lpg), inv, eps));
+        if (turn < mine) {
 #pragma unroll
             for (int c = 0; c < CPL; c++) {
-#pragma unroll
-                for (int i = 0; i < V; i++)
-                    f[c][i] = activate<T, Silu>(fmaf(f[c][i] * r, wc[c][i], bc[c][i]));
-                if (has[c])
-                    st_stream(y + n * d.yn + t.at + c * d.lpg * V, Elt<T>::narrow(f[c]));
+                const Vals<V> z = fma(mul(f[c], Vals<V>::splat(r)), wc[c], bc[c]);
+                if (has[c]) store_v<T, V>(o + c * d.lpg * V, activate<T, Silu, V>(z));
             }
             if (t.on && t.j == 0) {
                 mean[n * d.G + t.g] = m;
                 rstd[n * d.G + t.g] = r;
             }
         }
+        n += d.step;
+        o += d.ystep;
     }
     pdl_trigger();
 }
 
 template <typename T, int CPL, bool Silu>
-__global__ void __launch_bounds__(RT, 2)
+__global__ void __launch_bounds__(RT, CPL == 1 ? 3 : 2)
     gn_rows_bwd_kernel(const T* x, const T* dy, T* dx, const float* w, const float* b,
                        const float* mean, const float* rstd, float* part_a, float* part_b,
                        const RowShape d) {
-    constexpr int V = Elt<T>::V, U = CPL == 1 ? 2 : 1;
+    constexpr int V = Elt<T>::V, S = CPL == 1 ? kBwdStages : kBwdStages / 2;
     extern __shared__ float4 smem[];
-    float* sum = reinterpret_cast<float*>(smem);  // [2][RW][CPL][V][32]
+    float* sum = reinterpret_cast<float*>(smem);  // [2][RW][CPL][V][32], in place of the staging
     const Place t(d, V);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const float inv = 1.0f / (float)d.Cg;
     bool has[CPL];
-    float wc[CPL][V], bc[CPL][V], A[CPL][V], B[CPL][V];
+    Vals<V> wc[CPL], bc[CPL], A[CPL], B[CPL];
     pdl_wait();
 #pragma unroll
     for (int c = 0; c < CPL; c++) {
         has[c] = t.on && t.j + c * d.lpg < d.cpg;
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-            wc[c][i] = has[c] ? __ldg(w + t.at + c * d.lpg * V + i) : 0.f;
-            bc[c][i] = has[c] ? __ldg(b + t.at + c * d.lpg * V + i) : 0.f;
-            A[c][i] = B[c][i] = 0.f;
+        wc[c] = bc[c] = A[c] = B[c] = Vals<V>::splat(0.f);
+        if (has[c]) {
+            wc[c] = params<V>(w, t.at + c * d.lpg * V);
+            bc[c] = params<V>(b, t.at + c * d.lpg * V);
         }
     }
-    const int64_t step = (int64_t)d.RB * RW * d.rpw;
-    const int64_t first = ((int64_t)(blockIdx.x / d.segs) * RW + wid) * d.rpw;
-    for (int64_t n0 = first; n0 < d.N; n0 += U * step) {
-        Raw16 rx[U][CPL], rg[U][CPL];
-        float mu[U], rs[U];
+    int64_t n = ((int64_t)(blockIdx.x / d.segs) * RW + wid) * d.rpw;
+    const int turns = n < d.N ? (int)((d.N - 1 - n) / d.step) + 1 : 0;  // of the warp
+    n += t.sub;
+    const int mine = n < d.N ? (int)((d.N - 1 - n) / d.step) + 1 : 0;   // of the lane
+    Walk<T, V, 2 * CPL, S> in;
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int64_t n = n0 + u * step + t.sub;
-            const bool in = t.on && n < d.N;
-#pragma unroll
-            for (int c = 0; c < CPL; c++) {
-                const bool h = has[c] && n < d.N;
-                const int64_t at = t.at + c * d.lpg * V;
-                rx[u][c] = h ? ld_stream(x + n * d.xn + at) : raw_zero();
-                rg[u][c] = h ? ld_stream(dy + n * d.gn + at) : raw_zero();
-            }
-            mu[u] = in ? mean[n * d.G + t.g] : 0.f;
-            rs[u] = in ? rstd[n * d.G + t.g] : 0.f;
+    for (int c = 0; c < CPL; c++) {
+        const int at = has[c] ? t.at + c * d.lpg * V : 0;
+        in.p[2 * c] = x + n * d.xn + at;
+        in.p[2 * c + 1] = dy + n * d.gn + at;
+        in.step[2 * c] = d.xstep;
+        in.step[2 * c + 1] = d.gstep;
+        in.use[2 * c] = in.use[2 * c + 1] = has[c];
+    }
+    in.start(smem, mine);
+    T* o = dx + n * d.yn + t.at;
+    // the statistics, a turn ahead
+    const float *mp = mean + (mine ? n : 0) * d.G + t.g, *rp = rstd + (mine ? n : 0) * d.G + t.g;
+    float mu = __ldg(mp), rs = __ldg(rp);
+    GN_WALK(in, i, turns) {
+        const int turn = gn_j + i;
+        Held<T, V> h[2 * CPL];
+        in.next(i, h);
+        const float m0 = mu, r0 = rs;
+        if (turn + 1 < mine) {
+            mp += d.step * d.G;
+            rp += d.step * d.G;
+            mu = __ldg(mp);
+            rs = __ldg(rp);
         }
+        Vals<V> xh[CPL], g[CPL], s1 = Vals<V>::splat(0.f), s2 = s1;
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (n0 + u * step >= d.N) break;
-            const int64_t n = n0 + u * step + t.sub;
-            float xh[CPL][V], g[CPL][V], m1 = 0.f, m2 = 0.f;
+        for (int c = 0; c < CPL; c++) {
+            // absent lanes: dy = 0 keeps them out of every sum
+            if (d.rpw > 1 && turn >= mine) h[2 * c].raw = h[2 * c + 1].raw = raw_zero();
+            xh[c] = fma(h[2 * c].widen(), Vals<V>::splat(r0), Vals<V>::splat(-m0 * r0));
+            const Vals<V> dz = through<T, Silu, V>(h[2 * c + 1].widen(), fma(xh[c], wc[c], bc[c]));
+            A[c] = fma(dz, xh[c], A[c]);
+            B[c] = add(B[c], dz);
+            g[c] = mul(dz, wc[c]);
+            s1 = add(s1, g[c]);
+            s2 = fma(g[c], xh[c], s2);
+        }
+        float m1 = total(s1), m2 = total(s2);
+        lanes_sum2(m1, m2, d.lpg);
+        if (turn < mine) {
+            const Vals<V> r = Vals<V>::splat(r0), e1 = Vals<V>::splat(-r0 * inv * m1);
+            const Vals<V> e2 = Vals<V>::splat(-r0 * inv * m2);
 #pragma unroll
-            for (int c = 0; c < CPL; c++) {
-                Elt<T>::widen(rx[u][c], xh[c]);
-                Elt<T>::widen(rg[u][c], g[c]);
-#pragma unroll
-                for (int i = 0; i < V; i++) {
-                    // absent lanes hold zeros: dy = 0 keeps them out of every sum
-                    xh[c][i] = (xh[c][i] - mu[u]) * rs[u];
-                    const float dz = through<T, Silu>(g[c][i], fmaf(xh[c][i], wc[c][i], bc[c][i]));
-                    A[c][i] = fmaf(dz, xh[c][i], A[c][i]);
-                    B[c][i] += dz;
-                    g[c][i] = dz * wc[c][i];
-                    m1 += g[c][i];
-                    m2 = fmaf(g[c][i], xh[c][i], m2);
-                }
-            }
-            m1 = lanes_sum(m1, d.lpg) * inv;
-            m2 = lanes_sum(m2, d.lpg) * inv;
-            if (n >= d.N) continue;
-#pragma unroll
-            for (int c = 0; c < CPL; c++) {
-#pragma unroll
-                for (int i = 0; i < V; i++)
-                    g[c][i] = rs[u] * (g[c][i] - m1 - xh[c][i] * m2);
+            for (int c = 0; c < CPL; c++)
                 if (has[c])
-                    st_stream(dx + n * d.yn + t.at + c * d.lpg * V, Elt<T>::narrow(g[c]));
-            }
+                    store_v<T, V>(o + c * d.lpg * V, fma(g[c], r, fma(xh[c], e2, e1)));
         }
+        o += d.ystep;
     }
+    __syncthreads();
     // the block's sums, over its warps and a warp's rows in order
 #pragma unroll
-    for (int c = 0; c < CPL; c++)
+    for (int c = 0; c < CPL; c++) {
+        float fa[V], fb[V];
+        A[c].to(fa);
+        B[c].to(fb);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            sum[((wid * CPL + c) * V + i) * 32 + lane] = A[c][i];
-            sum[(((RW + wid) * CPL + c) * V + i) * 32 + lane] = B[c][i];
+            sum[((wid * CPL + c) * V + i) * 32 + lane] = fa[i];
+            sum[(((RW + wid) * CPL + c) * V + i) * 32 + lane] = fb[i];
         }
+    }
     __syncthreads();
     if (t.on && t.sub == 0) {
         const int64_t row = (int64_t)(blockIdx.x / d.segs) * d.C;
@@ -734,34 +932,51 @@ __global__ void __launch_bounds__(RT, 2)
     pdl_trigger();
 }
 
-// Row tiles of a sample: as many as give a chunk of samples about eight blocks
-// an SM, of 16 KB to 256 KB each and at most 304 a sample (every block of the
-// second pass reads its sample's tiles' statistics).  chunk: samples of one
-// pair of passes, whose tensors (x, or x and dy) fit in L2.
+// Cut a sample into row tiles: as many as give the chunk at most `blocks`
+// blocks (a number that the SMs hold at once, so that none waits for a second
+// turn), of 16 KB or more each.
+void tile(Shape& d, int64_t chunk, int64_t blocks, int es) {
+    const int64_t most = std::max<int64_t>(1, blocks / chunk);
+    int64_t rows = std::max<int64_t>(1, (16 << 10) / ((int64_t)d.C * es));
+    rows = std::max(rows, (d.S + most - 1) / most);
+    d.rows = rows;
+    d.tiles = (int)((d.S + rows - 1) / rows);
+}
+
+constexpr int64_t kStatsBlocks = kDesignSMs * 4, kBlocks = kDesignSMs * 3;
+
+// chunk: samples of one pair of passes, whose tensors (x, or x and dy) fit in
+// L2.  The tiles are the first pass's.
 constexpr int64_t kL2Chunk = 64 << 20;
 
-Shape shape_of(int64_t N, int64_t S, int64_t C, int64_t G, int es, int tensors, int64_t& chunk) {
+Shape shape_of(int64_t N, int64_t S, int64_t C, int64_t G, int es, bool backward, int64_t& chunk) {
     Shape d{};
     d.S = S;
     d.C = (int)C;
     d.G = (int)G;
     d.Cg = (int)(C / G);
-    const int64_t row = C * es, sample = S * row * tensors;
+    const int64_t sample = S * C * es * (backward ? 2 : 1);
     chunk = std::min(N, std::max<int64_t>(1, kL2Chunk / sample));
+    chunk = (N + (N + chunk - 1) / chunk - 1) / ((N + chunk - 1) / chunk);  // even chunks
     d.N = chunk;
-    int64_t bytes = chunk * (S * row) / (kDesignSMs * 8);
-    bytes = std::max<int64_t>(16 << 10, std::min<int64_t>(256 << 10, bytes));
-    int64_t rows = std::max<int64_t>(1, bytes / row);
-    rows = std::max(rows, (S + 303) / 304);
-    const int64_t tiles = (S + rows - 1) / rows;
-    d.rows = (S + tiles - 1) / tiles;
-    d.tiles = (int)((S + d.rows - 1) / d.rows);
+    tile(d, chunk, backward ? kBlocks : kStatsBlocks, es);
+    d.joins = d.tiles > kJoin ? 1 : d.tiles;
+    d.jrows = d.tiles > kJoin ? S : d.rows;
+    d.lg = 32;
+    while (d.lg > 1 && NT / d.lg < d.G) d.lg /= 2;
     return d;
+}
+
+// Rows that lie between the ones of a thread.
+void steps(Shape& d, int V) {
+    const int cv = d.C / V;
+    const int64_t RL = cv < NT ? NT / cv : 1;
+    d.xstep = RL * d.xs, d.ystep = RL * d.ys, d.gstep = RL * d.gs;
 }
 
 // Blocks of the backward's first pass: rows of the channels' partial sums.
 int64_t grad_rows(const Shape& d) {
-    return std::min<int64_t>(d.N * d.tiles, kDesignSMs * 8);
+    return std::min<int64_t>(d.N * d.tiles, kBlocks);
 }
 
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
@@ -773,7 +988,7 @@ size_t lanes_bytes(int C, int V) {
 
 template <typename K>
 cudaError_t allow(K kernel, size_t smem) {
-    return smem <= 48 * 1024 ? cudaSuccess
+    return smem <= 40 * 1024 ? cudaSuccess
                              : cudaFuncSetAttribute((const void*)kernel,
                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                     (int)smem);
@@ -781,7 +996,7 @@ cudaError_t allow(K kernel, size_t smem) {
 
 // Whether S == 1 rows take the row kernels, and their shape: 16-byte vectors
 // that no group shares, at most 64 of them a group.
-bool row_shape(int64_t N, int64_t S, int64_t C, int64_t G, int es, RowShape& d) {
+bool row_shape(int64_t N, int64_t S, int64_t C, int64_t G, int es, bool backward, RowShape& d) {
     const int V = 16 / es;
     const int64_t Cg = C / G;
     if (S != 1 || N == 0 || Cg % V || Cg / V > 64) return false;
@@ -797,18 +1012,23 @@ bool row_shape(int64_t N, int64_t S, int64_t C, int64_t G, int es, RowShape& d) 
     d.spr = d.G * d.lpg;
     d.rpw = d.spr < 32 ? 32 / d.spr : 1;
     d.segs = (d.spr + 31) / 32;
-    // blocks along the samples: four an SM, fewer where warps would stand idle
+    // blocks along the samples: as many as the SMs hold at once, fewer where
+    // warps would stand idle
     const int64_t per = (int64_t)RW * d.rpw, need = (N + per - 1) / per;
-    const int64_t most = kDesignSMs * 4 / d.segs;
+    const int64_t most = kDesignSMs * (cpl == 2 ? 2 : backward ? 3 : 4) / d.segs;
     d.RB = (int)(need < most ? need : most < 1 ? 1 : most);
+    d.step = (int64_t)d.RB * per;
     return true;
 }
 
 template <typename T, int CPL>
 cudaError_t rows_fwd(const GroupNormFwd& a, const RowShape& d, bool silu, cudaStream_t s) {
-    return launch(silu ? gn_rows_fwd_kernel<T, CPL, true> : gn_rows_fwd_kernel<T, CPL, false>,
-                  dim3((unsigned)(d.segs * d.RB)), dim3(RT), 0, s, true, (const T*)a.x, (T*)a.y,
-                  a.w, a.b, a.eps, a.mean, a.rstd, d);
+    const auto k = silu ? gn_rows_fwd_kernel<T, CPL, true> : gn_rows_fwd_kernel<T, CPL, false>;
+    constexpr size_t smem = Walk<T, Elt<T>::V, CPL, kFwdStages>::bytes;
+    const cudaError_t e = allow(k, smem);
+    if (e != cudaSuccess) return e;
+    return launch(k, dim3((unsigned)(d.segs * d.RB)), dim3(RT), smem, s, true, (const T*)a.x,
+                  (T*)a.y, a.w, a.b, a.eps, a.mean, a.rstd, d);
 }
 
 template <typename T, int CPL>
@@ -816,7 +1036,8 @@ cudaError_t rows_bwd(const GroupNormBwd& a, const RowShape& d, bool silu, cudaSt
     float* pa = (float*)a.workspace;
     float* pb = pa + pad64((int64_t)d.RB * d.C);
     const auto k = silu ? gn_rows_bwd_kernel<T, CPL, true> : gn_rows_bwd_kernel<T, CPL, false>;
-    const size_t smem = (size_t)2 * RW * CPL * Elt<T>::V * 32 * 4;
+    constexpr size_t stage = Walk<T, Elt<T>::V, 2 * CPL, CPL == 1 ? kBwdStages : kBwdStages / 2>::bytes;
+    constexpr size_t smem = std::max(stage, (size_t)2 * RW * CPL * Elt<T>::V * 32 * 4);
     cudaError_t e = allow(k, smem);
     if (e == cudaSuccess)
         e = launch(k, dim3((unsigned)(d.segs * d.RB)), dim3(RT), smem, s, true, (const T*)a.x,
@@ -827,21 +1048,37 @@ cudaError_t rows_bwd(const GroupNormBwd& a, const RowShape& d, bool silu, cudaSt
                   a.accumulate);
 }
 
+dim3 join_grid(const Shape& d) { return dim3((unsigned)((d.N * d.G + NT / 32 - 1) / (NT / 32))); }
+
+// Partial statistics of a chunk's tiles, and of its samples.
+int64_t part_floats(const Shape& d, int64_t chunk) { return pad64(2 * chunk * (d.tiles + 1) * d.G); }
+
 template <typename T, int V>
 cudaError_t fwd(const GroupNormFwd& a, Shape d, int64_t chunk, bool silu, cudaStream_t s) {
     float2* part = (float2*)a.workspace;
-    const size_t smem = 2 * lanes_bytes(d.C, V), smem2 = (size_t)d.G * 8;
+    constexpr size_t stage = Walk<T, V, 1, kFwdStages>::bytes;
+    const size_t smem = stage + 2 * lanes_bytes(d.C, V), smem2 = stage + (size_t)d.G * 8;
     const auto apply = silu ? gn_apply_kernel<T, V, true> : gn_apply_kernel<T, V, false>;
     cudaError_t e = allow(gn_stats_kernel<T, V>, smem);
     if (e == cudaSuccess) e = allow(apply, smem2);
+    steps(d, V);
+    Shape d2 = d;
+    tile(d2, chunk, kBlocks, (int)sizeof(T));
     for (int64_t n = 0; n < a.N && e == cudaSuccess; n += chunk) {
-        d.N = std::min(chunk, a.N - n);
-        const dim3 grid((unsigned)(d.N * d.tiles));
+        d.N = d2.N = std::min(chunk, a.N - n);
         const T* x = (const T*)a.x + n * d.xn;
-        e = launch(gn_stats_kernel<T, V>, grid, dim3(NT), smem, s, true, x, d, part);
+        e = launch(gn_stats_kernel<T, V>, dim3((unsigned)(d.N * d.tiles)), dim3(NT), smem, s, true,
+                   x, d, part);
+        const float2* p = part;
+        if (e == cudaSuccess && d.joins < d.tiles) {
+            float2* joined = part + chunk * d.tiles * d.G;
+            e = launch(gn_join_kernel<false>, join_grid(d), dim3(NT), 0, s, true, p, joined, d);
+            p = joined;
+        }
         if (e == cudaSuccess)
-            e = launch(apply, grid, dim3(NT), smem2, s, true, x, (T*)a.y + n * d.yn, a.w, a.b,
-                       a.eps, a.mean + n * d.G, a.rstd + n * d.G, (const float2*)part, d);
+            e = launch(apply, dim3((unsigned)(d2.N * d2.tiles)), dim3(NT), smem2, s, true, x,
+                       (T*)a.y + n * d.yn, a.w, a.b, a.eps, a.mean + n * d.G, a.rstd + n * d.G, p,
+                       d2);
     }
     return e;
 }
@@ -852,11 +1089,13 @@ cudaError_t bwd(const GroupNormBwd& a, Shape d, int64_t chunk, bool silu, cudaSt
     float* pa = (float*)a.workspace;
     float* pb = pa + pad64(chunks * P * d.C);
     float2* pg = (float2*)(pb + pad64(chunks * P * d.C));
-    const size_t smem = 2 * lanes_bytes(d.C, V), smem2 = (size_t)d.G * 16;
+    constexpr size_t stage = Walk<T, V, 2, kBwdStages>::bytes;
+    const size_t smem = stage + 2 * lanes_bytes(d.C, V), smem2 = stage + (size_t)d.G * 16;
     const auto sums = silu ? gn_bwd_sums_kernel<T, V, true> : gn_bwd_sums_kernel<T, V, false>;
     const auto apply = silu ? gn_bwd_apply_kernel<T, V, true> : gn_bwd_apply_kernel<T, V, false>;
     cudaError_t e = allow(sums, smem);
     if (e == cudaSuccess) e = allow(apply, smem2);
+    steps(d, V);
     int64_t rows = 0;
     for (int64_t n = 0; n < a.N && e == cudaSuccess; n += chunk) {
         d.N = std::min(chunk, a.N - n);
@@ -865,9 +1104,15 @@ cudaError_t bwd(const GroupNormBwd& a, Shape d, int64_t chunk, bool silu, cudaSt
         const float *mean = a.mean + n * d.G, *rstd = a.rstd + n * d.G;
         e = launch(sums, dim3((unsigned)p), dim3(NT), smem, s, true, x, dy, a.w, a.b, mean, rstd, d,
                    pg, pa + rows * d.C, pb + rows * d.C);
+        const float2* q = pg;
+        if (e == cudaSuccess && d.joins < d.tiles) {
+            float2* joined = pg + (int64_t)chunk * d.tiles * d.G;
+            e = launch(gn_join_kernel<true>, join_grid(d), dim3(NT), 0, s, true, q, joined, d);
+            q = joined;
+        }
         if (e == cudaSuccess)
             e = launch(apply, dim3((unsigned)(d.N * d.tiles)), dim3(NT), smem2, s, true, x, dy,
-                       (T*)a.dx + n * d.yn, a.w, a.b, mean, rstd, (const float2*)pg, d);
+                       (T*)a.dx + n * d.yn, a.w, a.b, mean, rstd, q, d);
         rows += p;
     }
     if (e != cudaSuccess) return e;
@@ -880,33 +1125,34 @@ cudaError_t bwd(const GroupNormBwd& a, Shape d, int64_t chunk, bool silu, cudaSt
 int64_t groupnorm_fwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
     if (N == 0 || S == 0 || C == 0) return 0;
     int64_t chunk;
-    const Shape d = shape_of(N, S, C, G, elt_bytes(dtype), 1, chunk);
-    return pad64(2 * chunk * d.tiles * G);
+    const Shape d = shape_of(N, S, C, G, elt_bytes(dtype), false, chunk);
+    return part_floats(d, chunk);
 }
 
 int64_t groupnorm_bwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
     if (N == 0 || S == 0 || C == 0) return 0;
     int64_t chunk;
-    const Shape d = shape_of(N, S, C, G, elt_bytes(dtype), 2, chunk);
+    const Shape d = shape_of(N, S, C, G, elt_bytes(dtype), true, chunk);
     const int64_t chunks = (N + chunk - 1) / chunk;
-    int64_t n = 2 * pad64(chunks * grad_rows(d) * C) + pad64(2 * chunk * d.tiles * G);
+    int64_t n = 2 * pad64(chunks * grad_rows(d) * C) + part_floats(d, chunk);
     RowShape r;  // taken or not by the pointers' alignment
-    if (row_shape(N, S, C, G, elt_bytes(dtype), r)) n = std::max(n, 2 * pad64((int64_t)r.RB * C));
+    if (row_shape(N, S, C, G, elt_bytes(dtype), true, r)) n = std::max(n, 2 * pad64((int64_t)r.RB * C));
     return n;
 }
 
 cudaError_t launch_groupnorm_fwd(const GroupNormFwd& a, cudaStream_t s) {
     const int es = elt_bytes(a.dtype);
     int64_t k;
-    Shape d = shape_of(a.N, a.S, a.C, a.G, es, 1, k);
+    Shape d = shape_of(a.N, a.S, a.C, a.G, es, false, k);
     d.xn = a.x_n, d.xs = a.x_s, d.yn = a.y_n, d.ys = a.y_s;
     const uint64_t bits = (uint64_t)a.C * es | (uint64_t)(uintptr_t)a.x | (uint64_t)(uintptr_t)a.y |
                           (a.N > 1 ? (uint64_t)(a.x_n | a.y_n) * es : 0) |
                           (a.S > 1 ? (uint64_t)(a.x_s | a.y_s) * es : 0);
     const bool vec = bits % 16 == 0, silu = a.act != 0;
     RowShape r;
-    if (vec && row_shape(a.N, a.S, a.C, a.G, es, r)) {
+    if (vec && row_shape(a.N, a.S, a.C, a.G, es, false, r)) {
         r.xn = a.x_n, r.yn = a.y_n;
+        r.xstep = r.step * r.xn, r.ystep = r.step * r.yn;
         if (r.cpg > 32)
             return a.dtype == 0   ? rows_fwd<float, 2>(a, r, silu, s)
                    : a.dtype == 1 ? rows_fwd<__half, 2>(a, r, silu, s)
@@ -927,7 +1173,7 @@ cudaError_t launch_groupnorm_bwd(const GroupNormBwd& a, cudaStream_t s) {
                       (const float*)nullptr, (const float*)nullptr, (int64_t)0, (int)a.C, a.grad_w,
                       a.grad_b, a.accumulate);
     int64_t k;
-    Shape d = shape_of(a.N, a.S, a.C, a.G, es, 2, k);
+    Shape d = shape_of(a.N, a.S, a.C, a.G, es, true, k);
     d.xn = a.x_n, d.xs = a.x_s, d.yn = a.dx_n, d.ys = a.dx_s, d.gn = a.dy_n, d.gs = a.dy_s;
     const uint64_t bits = (uint64_t)a.C * es | (uint64_t)(uintptr_t)a.x |
                           (uint64_t)(uintptr_t)a.dx | (uint64_t)(uintptr_t)a.dy |
@@ -935,8 +1181,9 @@ cudaError_t launch_groupnorm_bwd(const GroupNormBwd& a, cudaStream_t s) {
                           (a.S > 1 ? (uint64_t)(a.x_s | a.dx_s | a.dy_s) * es : 0);
     const bool vec = bits % 16 == 0, silu = a.act != 0;
     RowShape r;
-    if (vec && row_shape(a.N, a.S, a.C, a.G, es, r)) {
+    if (vec && row_shape(a.N, a.S, a.C, a.G, es, true, r)) {
         r.xn = a.x_n, r.yn = a.dx_n, r.gn = a.dy_n;
+        r.xstep = r.step * r.xn, r.ystep = r.step * r.yn, r.gstep = r.step * r.gn;
         if (r.cpg > 32)
             return a.dtype == 0   ? rows_bwd<float, 2>(a, r, silu, s)
                    : a.dtype == 1 ? rows_bwd<__half, 2>(a, r, silu, s)
