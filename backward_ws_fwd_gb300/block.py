@@ -6,10 +6,11 @@ checked here (TypeError, ValueError); the rest is checked there (WsfError).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
-from . import SIZE_MAX, _check, _dtype_code, _on, _ptr, _scratch, _stream, lib
+from . import SIZE_MAX, _check, _dtype_code, _scratch, lib
 
 _vp, _i64, _int, _sz, _f = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t,
                             ctypes.c_float)
@@ -37,28 +38,67 @@ lib.groupnorm_bwd.argtypes = [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i
 lib.groupnorm_bwd.restype = _int
 
 
-def _want(t, name, dtype, shape, like):
-    """t is a contiguous tensor of this type and shape on like's device."""
-    if t.dtype != dtype:
+# The checks of a call are one condition; only where it fails is the reason
+# looked for (a call of a few microseconds' work would otherwise spend more on
+# them than on the launch).
+
+def _fits(t, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on device dev."""
+    return t.dtype == dtype and t.shape == shape and t.device == dev and t.is_contiguous()
+
+
+def _along(t, x):
+    """t has x's type, shape and device, and unit inner stride."""
+    return (t.dtype == x.dtype and t.shape == x.shape and t.device == x.device and
+            (t.stride(-1) == 1 or t.shape[-1] <= 1))
+
+
+def _refuse(t, name, dtype, shape, dev):
+    """Raise what is wrong with t; dtype, shape None: any."""
+    if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not {dev}")
+    raise ValueError(f"{name} must be contiguous, or have unit inner stride")
+
+
+def _want(t, name, dtype, shape, dev):
+    if not _fits(t, dtype, shape, dev):
+        _refuse(t, name, dtype, shape, dev)
 
 
 def _like(t, name, x):
-    """t has x's type, shape and device and unit inner stride."""
-    if t.dtype != x.dtype:
-        raise TypeError(f"{name} must be {x.dtype}, not {t.dtype}")
-    if t.shape != x.shape:
-        raise ValueError(f"{name} must be {list(x.shape)}, not {list(t.shape)}")
-    if t.device != x.device:
-        raise ValueError(f"{name} is on {t.device}, not {x.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have unit inner stride")
+    if not _along(t, x):
+        _refuse(t, name, x.dtype, x.shape, x.device)
+
+
+def _at(stream, t):
+    """Context that makes t's device current, and the raw stream to launch on."""
+    import torch
+    dev = t.get_device()
+    if dev < 0:  # host memory: the library or CUDA refuses it
+        return contextlib.nullcontext(), None
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return (_HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)), raw
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _p(t):
+    """Address of t's data, None where it has none."""
+    return t.data_ptr() if t is not None and t.numel() else None
+
+
+def _work(need, workspace, t, stream):
+    """(address, bytes) of the caller's workspace, or of a temporary one."""
+    if workspace is None and need not in (0, SIZE_MAX):
+        workspace = _scratch(need, t.device, stream)
+    if workspace is None:
+        return None, 0, None
+    return _p(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
 # ---------------------------------------------------------------------------
@@ -71,45 +111,52 @@ def _strides3(t):
 
 def _rotary(call, what, q, k, positions, inv_freq, scale, interleaved, q_out, k_out, stream):
     import torch
-    if q.dim() not in (3, 4):
+    shape = q.shape
+    if len(shape) == 4:
+        B, S, H, D = shape
+    elif len(shape) == 3:
+        B, (S, H, D) = 1, shape
+    else:
         raise ValueError("heads must be [B, S, H, D] or [T, H, D]")
-    B, S = (q.shape[0], q.shape[1]) if q.dim() == 4 else (1, q.shape[0])
-    H, D = q.shape[-2:]
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dev, code = q.device, _dtype_code(q)
     _like(q, "q", q)
-    _like(q_out, "q_out", q)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    else:
+        _like(q_out, "q_out", q)
     R = 2 * inv_freq.numel()
-    _want(inv_freq, "inv_freq", torch.float32, (R // 2,), q)
+    _want(inv_freq, "inv_freq", torch.float32, (R // 2,), dev)
     Hk = 0
     if k is not None:
-        if k.shape[:-2] != q.shape[:-2] or k.shape[-1] != D:
-            raise ValueError(f"k {list(k.shape)} does not go with q {list(q.shape)}")
         Hk = k.shape[-2]
+        if k.shape[:-2] != shape[:-2] or k.shape[-1] != D:
+            raise ValueError(f"k {list(k.shape)} does not go with q {list(shape)}")
+        if k.dtype != q.dtype or k.device != dev or (k.stride(-1) != 1 and D > 1):
+            _refuse(k, "k", q.dtype, None, dev)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        if k.dtype != q.dtype or k.device != q.device:
-            raise TypeError("k must have q's type and device")
-        _like(k, "k", k)
-        _like(k_out, "k_out", k)
+            k_out = torch.empty_like(k)
+        else:
+            _like(k_out, "k_out", k)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    pb = {torch.int32: 4, torch.int64: 8}.get(positions.dtype)
-    if pb is None:
+    pb = 8 if positions.dtype == torch.int64 else 4
+    ps = positions.shape
+    ldp = 0
+    if len(ps) == 2 and ps[0] == B and ps[1] == S and len(shape) == 4:
+        ldp = positions.stride(0) if B > 1 else 0
+    elif ps != (S,) and not (len(shape) == 4 and ps == (1, S)):
+        raise ValueError(f"positions {list(ps)} do not go with q {list(shape)}")
+    if pb == 4 and positions.dtype != torch.int32:
         raise TypeError(f"positions must be int32 or int64, not {positions.dtype}")
-    if positions.device != q.device:
-        raise ValueError(f"positions are on {positions.device}, not {q.device}")
-    ps = tuple(positions.shape)
-    if ps != (S,) and (q.dim() == 3 or ps not in ((B, S), (1, S))):
-        raise ValueError(f"positions {list(ps)} do not go with q {list(q.shape)}")
-    if S > 1 and positions.stride(-1) != 1:
-        raise ValueError("positions must have unit inner stride")
-    ldp = positions.stride(0) if ps == (B, S) and len(ps) == 2 and B > 1 else 0
-    with _on(q):
-        _check(call(_ptr(q), _strides3(q), _ptr(q_out), _strides3(q_out), H, _ptr(k),
-                    _strides3(k) if Hk else None, _ptr(k_out), _strides3(k_out) if Hk else None,
-                    Hk, _ptr(positions), ldp, pb, _ptr(inv_freq), float(scale), int(interleaved),
-                    B, S, D, R, _dtype_code(q), _stream(stream, q.device)), what)
+    if positions.device != dev or (S > 1 and positions.stride(-1) != 1):
+        _refuse(positions, "positions", None, None, dev)
+    on, raw = _at(stream, q)
+    with on:
+        rc = call(_p(q), _strides3(q), _p(q_out), _strides3(q_out), H, _p(k),
+                  _strides3(k) if Hk else None, _p(k_out), _strides3(k_out) if Hk else None, Hk,
+                  _p(positions), ldp, pb, _p(inv_freq), scale, 1 if interleaved else 0, B, S, D,
+                  R, code, raw)
+    _check(rc, what)
     return q_out, k_out
 
 
@@ -187,37 +234,34 @@ def router_fwd(logits, k, mask=None, renormalize=False, gates=None, ids=None, co
     float32 [T, k], ids int32 [T, k], counts int32 [E], loss float32 [])."""
     import torch
     T, E = logits.shape
-    dev = logits.device
+    dev, code = logits.device, _dtype_code(logits)
     _like(logits, "logits", logits)
     if mask is not None:
-        if mask.dtype not in (torch.bool, torch.uint8):
+        if mask.dtype != torch.bool and mask.dtype != torch.uint8:
             raise TypeError("mask must be bool or uint8")
-        _want(mask, "mask", mask.dtype, (T,), logits)
+        _want(mask, "mask", mask.dtype, (T,), dev)
     if gates is None:
         gates = torch.empty((T, k), dtype=torch.float32, device=dev)
     else:
-        _want(gates, "gates", torch.float32, (T, k), logits)
+        _want(gates, "gates", torch.float32, (T, k), dev)
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     else:
-        _want(ids, "ids", torch.int32, (T, k), logits)
+        _want(ids, "ids", torch.int32, (T, k), dev)
     if counts is None:
         counts = torch.empty(E, dtype=torch.int32, device=dev)
     else:
-        _want(counts, "counts", torch.int32, (E,), logits)
+        _want(counts, "counts", torch.int32, (E,), dev)
     if loss is None:
         loss = torch.empty((), dtype=torch.float32, device=dev)
     else:
-        _want(loss, "loss", torch.float32, (), logits)
-    with _on(logits):
-        need = lib.router_fwd_workspace_bytes(T, E)
-        if workspace is None and need not in (0, SIZE_MAX):
-            workspace = _scratch(need, dev, stream)
-        wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(lib.router_fwd(_ptr(logits), logits.stride(0), _ptr(mask), k, int(bool(renormalize)),
-                              _ptr(gates), _ptr(ids), _ptr(counts), _ptr(loss), _ptr(workspace),
-                              wbytes, T, E, _dtype_code(logits), _stream(stream, dev)),
-               "router_fwd")
+        _want(loss, "loss", torch.float32, (), dev)
+    on, raw = _at(stream, logits)
+    with on:
+        ws, wbytes, keep = _work(lib.router_fwd_workspace_bytes(T, E), workspace, logits, stream)
+        rc = lib.router_fwd(_p(logits), logits.stride(0), _p(mask), k, 1 if renormalize else 0,
+                            _p(gates), _p(ids), _p(counts), _p(loss), ws, wbytes, T, E, code, raw)
+    _check(rc, "router_fwd")
     return gates, ids, counts, loss
 
 
@@ -226,23 +270,26 @@ def router_bwd(logits, ids, counts, dgates, dloss, renormalize=False, dlogits=No
     (float32 [T, k] or None) and dloss (float32 [] or None)."""
     import torch
     T, E = logits.shape
-    k = ids.shape[1]
+    dev, code = logits.device, _dtype_code(logits)
+    kept = ids.shape
+    k = kept[1]
     _like(logits, "logits", logits)
-    _want(ids, "ids", torch.int32, (T, k), logits)
-    _want(counts, "counts", torch.int32, (E,), logits)
+    _want(ids, "ids", torch.int32, (T, k), dev)
+    _want(counts, "counts", torch.int32, (E,), dev)
     if dgates is not None:
-        _want(dgates, "dgates", torch.float32, (T, k), logits)
+        _want(dgates, "dgates", torch.float32, kept, dev)
     if dloss is not None:
-        _want(dloss, "dloss", torch.float32, (), logits)
+        _want(dloss, "dloss", torch.float32, (), dev)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
     else:
         _like(dlogits, "dlogits", logits)
-    with _on(logits):
-        _check(lib.router_bwd(_ptr(logits), logits.stride(0), _ptr(ids), _ptr(counts), k,
-                              int(bool(renormalize)), _ptr(dgates), _ptr(dloss), _ptr(dlogits),
-                              dlogits.stride(0), T, E, _dtype_code(logits),
-                              _stream(stream, logits.device)), "router_bwd")
+    on, raw = _at(stream, logits)
+    with on:
+        rc = lib.router_bwd(_p(logits), logits.stride(0), _p(ids), _p(counts), k,
+                            1 if renormalize else 0, _p(dgates), _p(dloss), _p(dlogits),
+                            dlogits.stride(0), T, E, code, raw)
+    _check(rc, "router_bwd")
     return dlogits
 
 
@@ -261,10 +308,11 @@ def groupnorm_workspace_bytes(N: int, S: int, C: int, groups: int, dtype, backwa
 
 
 def _nsc(x):
-    if x.dim() == 3:
-        return x.shape
-    if x.dim() == 2:
-        return x.shape[0], 1, x.shape[1]
+    shape = x.shape
+    if len(shape) == 3:
+        return shape
+    if len(shape) == 2:
+        return shape[0], 1, shape[1]
     raise ValueError("x must be [N, S, C] or [N, C]")
 
 
@@ -287,31 +335,30 @@ def groupnorm_fwd(x, w, b, groups, eps=1e-5, act=None, y=None, mean=None, rstd=N
     "silu".  Returns (y, mean, rstd), the statistics float32 [N, groups]."""
     import torch
     N, S, C = _nsc(x)
-    code, act = _dtype_code(x), _act(act)
+    dev, code, act = x.device, _dtype_code(x), _act(act)
     _like(x, "x", x)
-    _want(w, "w", torch.float32, (C,), x)
-    _want(b, "b", torch.float32, (C,), x)
+    _want(w, "w", torch.float32, (C,), dev)
+    _want(b, "b", torch.float32, (C,), dev)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
         _like(y, "y", x)
     if mean is None:
-        mean = torch.empty((N, groups), dtype=torch.float32, device=x.device)
+        mean = torch.empty((N, groups), dtype=torch.float32, device=dev)
     else:
-        _want(mean, "mean", torch.float32, (N, groups), x)
+        _want(mean, "mean", torch.float32, (N, groups), dev)
     if rstd is None:
-        rstd = torch.empty((N, groups), dtype=torch.float32, device=x.device)
+        rstd = torch.empty((N, groups), dtype=torch.float32, device=dev)
     else:
-        _want(rstd, "rstd", torch.float32, (N, groups), x)
-    with _on(x):
-        need = lib.groupnorm_fwd_workspace_bytes(N, S, C, groups, code)
-        if workspace is None and need not in (0, SIZE_MAX):
-            workspace = _scratch(need, x.device, stream)
-        wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(lib.groupnorm_fwd(_ptr(x), *_ns_strides(x), _ptr(w), _ptr(b), float(eps), act,
-                                 _ptr(y), *_ns_strides(y), _ptr(mean), _ptr(rstd),
-                                 _ptr(workspace), wbytes, N, S, C, groups, code,
-                                 _stream(stream, x.device)), "groupnorm_fwd")
+        _want(rstd, "rstd", torch.float32, (N, groups), dev)
+    on, raw = _at(stream, x)
+    with on:
+        ws, wbytes, keep = _work(lib.groupnorm_fwd_workspace_bytes(N, S, C, groups, code),
+                                 workspace, x, stream)
+        rc = lib.groupnorm_fwd(_p(x), *_ns_strides(x), _p(w), _p(b), eps, act, _p(y),
+                               *_ns_strides(y), _p(mean), _p(rstd), ws, wbytes, N, S, C, groups,
+                               code, raw)
+    _check(rc, "groupnorm_fwd")
     return y, mean, rstd
 
 
@@ -321,33 +368,32 @@ def groupnorm_bwd(x, w, b, mean, rstd, dy, groups, act=None, dx=None, grad_w=Non
     statistics.  Returns (dx, grad_w, grad_b)."""
     import torch
     N, S, C = _nsc(x)
-    code, act = _dtype_code(x), _act(act)
+    dev, code, act = x.device, _dtype_code(x), _act(act)
     _like(x, "x", x)
     _like(dy, "dy", x)
-    _want(w, "w", torch.float32, (C,), x)
-    _want(b, "b", torch.float32, (C,), x)
-    _want(mean, "mean", torch.float32, (N, groups), x)
-    _want(rstd, "rstd", torch.float32, (N, groups), x)
+    _want(w, "w", torch.float32, (C,), dev)
+    _want(b, "b", torch.float32, (C,), dev)
+    _want(mean, "mean", torch.float32, (N, groups), dev)
+    _want(rstd, "rstd", torch.float32, (N, groups), dev)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
         _like(dx, "dx", x)
     if grad_w is None:
-        grad_w = torch.empty(C, dtype=torch.float32, device=x.device)
+        grad_w = torch.empty(C, dtype=torch.float32, device=dev)
     else:
-        _want(grad_w, "grad_w", torch.float32, (C,), x)
+        _want(grad_w, "grad_w", torch.float32, (C,), dev)
     if grad_b is None:
-        grad_b = torch.empty(C, dtype=torch.float32, device=x.device)
+        grad_b = torch.empty(C, dtype=torch.float32, device=dev)
     else:
-        _want(grad_b, "grad_b", torch.float32, (C,), x)
-    with _on(x):
-        need = lib.groupnorm_bwd_workspace_bytes(N, S, C, groups, code)
-        if workspace is None and need not in (0, SIZE_MAX):
-            workspace = _scratch(need, x.device, stream)
-        wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(lib.groupnorm_bwd(_ptr(x), *_ns_strides(x), _ptr(w), _ptr(b), _ptr(mean),
-                                 _ptr(rstd), _ptr(dy), *_ns_strides(dy), act, _ptr(dx),
-                                 *_ns_strides(dx), _ptr(grad_w), _ptr(grad_b),
-                                 int(bool(accumulate)), _ptr(workspace), wbytes, N, S, C, groups,
-                                 code, _stream(stream, x.device)), "groupnorm_bwd")
+        _want(grad_b, "grad_b", torch.float32, (C,), dev)
+    on, raw = _at(stream, x)
+    with on:
+        ws, wbytes, keep = _work(lib.groupnorm_bwd_workspace_bytes(N, S, C, groups, code),
+                                 workspace, x, stream)
+        rc = lib.groupnorm_bwd(_p(x), *_ns_strides(x), _p(w), _p(b), _p(mean), _p(rstd), _p(dy),
+                               *_ns_strides(dy), act, _p(dx), *_ns_strides(dx), _p(grad_w),
+                               _p(grad_b), 1 if accumulate else 0, ws, wbytes, N, S, C, groups,
+                               code, raw)
+    _check(rc, "groupnorm_bwd")
     return dx, grad_w, grad_b

@@ -15,12 +15,12 @@
 // A row is held by L lanes (8 consecutive experts a lane; rows wider than
 // 256 experts give each lane 2 or 4 such runs), 32/L rows a warp, so that
 // reductions over a row are log2 L shuffles shared by all of a warp's rows.
-// The k largest are taken one at a time: each lane's maximum of
-// order-preserving integer keys, a butterfly over the row's lanes, and the
-// winner's key cleared.  For 16-bit storage a key holds the value's 16 bits
-// above the complement of the expert's index, so that one integer maximum
-// also settles ties; binary32 carries the index beside the key.  The largest
-// is also the softmax's shift.
+// Every lane sorts its runs of order-preserving integer keys (19 comparators)
+// into shared memory; the k largest are then taken one at a time, the maximum
+// over the lanes' heads, whose owner steps on in its run.  For 16-bit storage
+// a key holds the value's 16 bits above the complement of the expert's index,
+// so that one integer maximum also settles ties; binary32 carries the index
+// beside the key.  The largest is also the softmax's shift.
 //
 // Σ_t p_te is summed in registers (every lane keeps its experts for all
 // rows), then over the block, into one partial row a block; a second kernel
@@ -54,29 +54,114 @@ __device__ __forceinline__ float ex2(float x) {
 // every logit is the type's lowest value.
 __device__ __forceinline__ float exp_of(float f, float m) { return ex2((f - m) * kLog2e); }
 
-// Integers in the order of the values (−0 as +0, NaN at the ends); 0 stands
-// for an expert that is taken or does not exist.  For 16-bit storage the low
-// half is the complement of the expert's index e < 2¹⁶ − 1.
-template <typename T>
-__device__ __forceinline__ uint32_t order_key(float f, int e) {
-    if constexpr (sizeof(T) == 4) {
-        const uint32_t b = __float_as_uint(f + 0.0f);
-        return max(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 1u);
-    } else {
-        uint32_t b;
-        if constexpr (std::is_same<T, __half>::value)
-            b = (uint32_t)__half_as_ushort(__float2half_rn(f + 0.0f)) << 16;
-        else
-            b = __float_as_uint(f + 0.0f);
-        b ^= (uint32_t)((int32_t)b >> 31) | 0x80000000u;
-        return (b & 0xffff0000u) | (uint32_t)(0xffff - e);
-    }
+// Index of element i of a lane's 8·R experts.
+template <int L>
+__device__ __forceinline__ int expert(int i, int sub) {
+    return ((i / 8) * L + sub) * 8 + i % 8;
 }
 
-// The value an order_key stands for.
+// A lane's 8·R logits of a row as they are stored (8 of a 16-bit type in 4
+// words, of binary32 in 8), −inf behind the last expert.  Rows of experts in
+// eights at 16-byte addresses (vec) are read and written 16 bytes at a time,
+// others element by element.
+template <typename T, int L, int R>
+struct Logits {
+    static constexpr int W = 8 * (int)sizeof(T) / 4;  // words of a run
+    uint32_t w[R * W];
+
+    __device__ __forceinline__ void load(const T* row, bool on, int sub, int E, bool vec) {
+        const uint32_t none = sizeof(T) == 4                     ? 0xff800000u
+                              : std::is_same<T, __half>::value ? 0xfc00fc00u
+                                                               : 0xff80ff80u;
+#pragma unroll
+        for (int i = 0; i < R * W; i++) w[i] = none;
+        if (!on) return;
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const int e0 = expert<L>(r * 8, sub);
+            if (vec) {
+                if (e0 < E) {
+#pragma unroll
+                    for (int h = 0; h < W / 4; h++) {
+                        const Raw16 q = ld_keep(row + e0 + h * Elt<T>::V);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) w[r * W + h * 4 + i] = q.u[i];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    if (e0 + i >= E) continue;
+                    if constexpr (sizeof(T) == 4) {
+                        w[r * W + i] = __ldg(reinterpret_cast<const uint32_t*>(row) + e0 + i);
+                    } else {
+                        const uint32_t v = __ldg(reinterpret_cast<const unsigned short*>(row) + e0 + i);
+                        uint32_t& d = w[r * W + i / 2];
+                        d = i & 1 ? (d & 0xffffu) | v << 16 : (d & 0xffff0000u) | v;
+                    }
+                }
+            }
+        }
+    }
+    // as binary32, two a register pair
+    __device__ __forceinline__ void widen(uint64_t (&f)[4 * R]) const {
+#pragma unroll
+        for (int i = 0; i < 4 * R; i++) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            } else if constexpr (std::is_same<T, __half>::value) {
+                __half2 h;
+                memcpy(&h, &w[i], 4);
+                const float2 v = __half22float2(h);
+                f[i] = f2_pack(v.x, v.y);
+            } else {
+                f[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+            }
+        }
+    }
+    // Integers in the order of the values (−0 as +0, NaN at the ends), with the
+    // complement of the expert's index in the low half for 16-bit types.  0 is
+    // below every key of an expert.
+    __device__ __forceinline__ void keys(int sub, int E, uint32_t (&key)[8 * R]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8 * R; i++) {
+                const uint32_t b = __float_as_uint(__uint_as_float(w[i]) + 0.0f);
+                key[i] = max(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 1u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4 * R; i++) {
+                uint32_t b;  // both halves + 0
+                if constexpr (std::is_same<T, __half>::value) {
+                    __half2 h;
+                    memcpy(&h, &w[i], 4);
+                    h = __hadd2(h, __float2half2_rn(0.f));
+                    memcpy(&b, &h, 4);
+                } else {
+                    __nv_bfloat162 h;
+                    memcpy(&h, &w[i], 4);
+                    h = __hadd2(h, __float2bfloat162_rn(0.f));
+                    memcpy(&b, &h, 4);
+                }
+                b ^= ((b >> 15 & 0x00010001u) * 0xffffu) | 0x80008000u;
+                const uint32_t c = 0xffffu - (uint32_t)expert<L>(2 * i, sub);
+                key[2 * i] = b * 65536u + c;
+                key[2 * i + 1] = (b & 0xffff0000u) | (c - 1u);
+            }
+        }
+        if (E < 8 * R * L) {
+#pragma unroll
+            for (int i = 0; i < 8 * R; i++)
+                if (expert<L>(i, sub) >= E) key[i] = 0u;
+        }
+    }
+};
+
+// The value a key stands for.
 template <typename T>
 __device__ __forceinline__ float key_value(uint32_t key) {
-    uint32_t b = key ^ (~(uint32_t)((int32_t)key >> 31) | 0x80000000u);
+    const uint32_t b = key ^ (~(uint32_t)((int32_t)key >> 31) | 0x80000000u);
     if constexpr (sizeof(T) == 4)
         return __uint_as_float(b);
     else if constexpr (std::is_same<T, __half>::value)
@@ -85,42 +170,327 @@ __device__ __forceinline__ float key_value(uint32_t key) {
         return __uint_as_float(b & 0xffff0000u);
 }
 
-// Index of element i of a lane's 8·R experts.
-template <int L>
-__device__ __forceinline__ int expert(int i, int sub) {
-    return ((i / 8) * L + sub) * 8 + i % 8;
-}
-
-// The lane's 8·R logits of a row as binary32, −inf behind the last expert.
-// Rows of experts in eights at 16-byte addresses (vec) are read and written
-// 16 bytes at a time, others element by element.
-template <typename T, int L, int R>
-__device__ __forceinline__ void load_row(const T* row, bool on, int sub, int E, bool vec,
-                                         float (&f)[8 * R]) {
-    constexpr int V = Elt<T>::V;
-#pragma unroll
-    for (int r = 0; r < R; r++) {
-        const int e0 = expert<L>(r * 8, sub);
-        if (vec) {
-#pragma unroll
-            for (int h = 0; h < 8; h += V) {
-                float g[V];
-                if (on && e0 < E) {
-                    Elt<T>::widen(ld_keep(row + e0 + h), g);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; i++) g[i] = ninf();
-                }
-#pragma unroll
-                for (int i = 0; i < V; i++) f[r * 8 + h + i] = g[i];
-            }
+// A key with its expert: for 16-bit types the key alone, for binary32 the pair
+// (ordered by key, then by the lower expert).
+template <typename T>
+struct Pick {
+    uint32_t key;
+    __device__ __forceinline__ static Pick of(uint32_t k, int) { return Pick{k}; }
+    __device__ __forceinline__ int id() const { return 0xffff - (int)(key & 0xffffu); }
+    __device__ __forceinline__ bool above(const Pick& o) const { return key > o.key; }
+    __device__ __forceinline__ bool same(const Pick& o) const { return key == o.key; }
+    __device__ __forceinline__ static void order(Pick& a, Pick& b) {
+        const uint32_t hi = max(a.key, b.key), lo = min(a.key, b.key);
+        a.key = hi, b.key = lo;
+    }
+    template <int L>
+    __device__ __forceinline__ Pick best() const {
+        uint32_t k = key;
+        if constexpr (L == 32) {
+            k = __reduce_max_sync(FULL_MASK, k);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                f[r * 8 + i] = on && e0 + i < E ? Elt<T>::load1(row + e0 + i) : ninf();
+            for (int o = L / 2; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(FULL_MASK, k, o));
+        }
+        return Pick{k};
+    }
+};
+template <>
+struct Pick<float> {
+    uint32_t key;
+    uint32_t low;  // complement of the expert's index
+    __device__ __forceinline__ static Pick of(uint32_t k, int e) { return Pick{k, ~(uint32_t)e}; }
+    __device__ __forceinline__ int id() const { return (int)~low; }
+    __device__ __forceinline__ bool above(const Pick& o) const {
+        return ((uint64_t)key << 32 | low) > ((uint64_t)o.key << 32 | o.low);
+    }
+    __device__ __forceinline__ bool same(const Pick& o) const { return low == o.low; }
+    __device__ __forceinline__ static void order(Pick& a, Pick& b) {
+        if (b.above(a)) {
+            const Pick t = a;
+            a = b;
+            b = t;
         }
     }
+    template <int L>
+    __device__ __forceinline__ Pick best() const {
+        Pick b = *this;
+        if constexpr (L == 32) {
+            b.key = __reduce_max_sync(FULL_MASK, key);
+            b.low = __reduce_max_sync(FULL_MASK, key == b.key ? low : 0u);
+        } else {
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) {
+                const Pick q{__shfl_xor_sync(FULL_MASK, b.key, o),
+                             __shfl_xor_sync(FULL_MASK, b.low, o)};
+                if (q.above(b)) b = q;
+            }
+        }
+        return b;
+    }
+};
+
+// Sort eight descending: Batcher's odd-even merge sort, 19 comparators.
+template <typename P>
+__device__ __forceinline__ void sort8(P* a) {
+#define CE(i, j) P::order(a[i], a[j])
+    CE(0, 1); CE(2, 3); CE(4, 5); CE(6, 7);
+    CE(0, 2); CE(1, 3); CE(4, 6); CE(5, 7);
+    CE(1, 2); CE(5, 6);
+    CE(0, 4); CE(1, 5); CE(2, 6); CE(3, 7);
+    CE(2, 4); CE(3, 5);
+    CE(1, 2); CE(3, 4); CE(5, 6);
+#undef CE
 }
+
+// ---------------------------------------------------------------------------
+struct FwdArgs {
+    const void* logits;
+    const unsigned char* mask;
+    float* gates;
+    int* ids;
+    float* part_p;  // [P, E]
+    int* part_c;    // [P, E]
+    int64_t ld;
+    int64_t T;
+    int E, k, renorm, vec;
+};
+
+// Shared memory: the sorted runs of every lane ([warp][run][place][lane]), the
+// chosen of every row, the counts; the warps' sums take the runs' place.
+template <typename T, int L, int R>
+size_t fwd_smem(int k) {
+    return (size_t)NT * 8 * R * sizeof(Pick<T>) + (size_t)NW * (32 / L) * k * sizeof(Pick<T>) +
+           (size_t)L * 8 * R * 4;
+}
+
+template <typename T, int L, int R>
+__global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
+    router_fwd_kernel(const FwdArgs a) {
+    using P = Pick<T>;
+    constexpr int EPL = 8 * R, RPW = 32 / L, SLOTS = L * EPL;
+    extern __shared__ float4 smem4[];
+    P* runs = reinterpret_cast<P*>(smem4);
+    P* took = runs + NT * EPL;
+    int* cnt = reinterpret_cast<int*>(took + NW * RPW * a.k);
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int sub = lane & (L - 1), grp = lane / L;
+    const int E = a.E, k = a.k;
+    P* run = runs + wid * 32 * EPL + lane;  // place q of run r: run[(r·8 + q)·32]
+    P* mine = took + (wid * RPW + grp) * k;
+
+    for (int i = threadIdx.x; i < SLOTS; i += NT) cnt[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    uint64_t sum_p[EPL / 2];
+#pragma unroll
+    for (int i = 0; i < EPL / 2; i++) sum_p[i] = f2_pack(0.f, 0.f);
+
+    const int64_t step = (int64_t)gridDim.x * NW * RPW;
+    int64_t row = ((int64_t)blockIdx.x * NW + wid) * RPW + grp;
+    Logits<T, L, R> next;
+    next.load((const T*)a.logits + row * a.ld, row < a.T, sub, E, a.vec);
+    bool keep = row < a.T && (!a.mask || a.mask[row]);
+    for (; row - grp < a.T; row += step) {
+        const Logits<T, L, R> x = next;
+        const bool on = row < a.T;
+        bool valid = keep;
+        // the next row is in flight meanwhile
+        next.load((const T*)a.logits + (row + step) * a.ld, row + step < a.T, sub, E, a.vec);
+        keep = row + step < a.T && (!a.mask || a.mask[row + step]);
+
+        // the k largest, in order: every lane sorts its runs and offers the
+        // first of what is left of them
+        uint32_t key[EPL];
+        x.keys(sub, E, key);
+        P head[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            P s[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++) s[q] = P::of(key[r * 8 + q], expert<L>(r * 8 + q, sub));
+            sort8(s);
+            head[r] = s[0];
+            if (k > 1) {
+#pragma unroll
+                for (int q = 1; q < 8; q++) run[(r * 8 + q) * 32] = s[q];
+            }
+        }
+        int at[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) at[r] = r * 256;  // the head's place, times 32
+        float m = 0.f;
+        for (int j = 0; j < k; j++) {
+            P b = head[0];
+#pragma unroll
+            for (int r = 1; r < R; r++)
+                if (head[r].above(b)) b = head[r];
+            b = b.template best<L>();
+            if (j == 0) m = key_value<T>(b.key);
+            if (sub == 0) mine[j] = b;
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                if (head[r].same(b)) {
+                    at[r] += 32;
+                    head[r] = P::of(0u, -1);
+                    if (at[r] < (r + 1) * 256) head[r] = run[at[r]];
+                }
+            }
+        }
+        valid = valid && m != ninf();  // no logit above −inf: the row does not count
+
+        // softmax, shifted by the largest
+        m = valid ? m : 0.f;
+        uint64_t f[EPL / 2];
+        x.widen(f);
+        const uint64_t m2 = f2_pack(m, m), l2 = f2_pack(kLog2e, kLog2e);
+        uint64_t z2 = f2_pack(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < EPL / 2; i++) {
+            float p, q;
+            f2_unpack(f2_mul(f2_sub(f[i], m2), l2), p, q);
+            f[i] = f2_pack(ex2(p), ex2(q));
+            z2 = f2_add(z2, f[i]);
+        }
+        float z, z1;
+        f2_unpack(z2, z, z1);
+        z = group_sum<L>(z + z1);
+        if (valid) {
+            const float inv = 1.0f / z;
+            const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+            for (int i = 0; i < EPL / 2; i++) sum_p[i] = f2_fma(f[i], inv2, sum_p[i]);
+        }
+
+        // gates and ids
+        __syncwarp();
+        if (a.renorm) {
+            z = 0.f;
+            for (int j = sub; j < k; j += L) z += exp_of(key_value<T>(mine[j].key), m);
+            z = group_sum<L>(z);
+        }
+        if (on) {
+            for (int j = sub; j < k; j += L) {
+                const P q = mine[j];
+                a.gates[row * k + j] = valid ? exp_of(key_value<T>(q.key), m) / z : 0.f;
+                a.ids[row * k + j] = valid ? q.id() : -1;
+                if (valid) atomicAdd(&cnt[q.id()], 1);
+            }
+        }
+        __syncwarp();
+    }
+
+    // the block's sums: over the warp's rows, then over the warps in order
+    __syncthreads();
+    float* ps = reinterpret_cast<float*>(smem4);  // [NW][SLOTS]
+#pragma unroll
+    for (int i = 0; i < EPL; i++) {
+        float u, v;
+        f2_unpack(sum_p[i / 2], u, v);
+        if (i & 1) u = v;
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) u += __shfl_xor_sync(FULL_MASK, u, o);
+        if (grp == 0) ps[wid * SLOTS + expert<L>(i, sub)] = u;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += NT) {
+        float v = ps[e];
+#pragma unroll
+        for (int w = 1; w < NW; w++) v += ps[w * SLOTS + e];
+        a.part_p[(int64_t)blockIdx.x * E + e] = v;
+        a.part_c[(int64_t)blockIdx.x * E + e] = cnt[e];
+    }
+    pdl_trigger();
+}
+
+// counts, and the loss, from the P partial rows: 32 columns by 32 stripes of
+// rows (p ≡ stripe mod 32, in order, then a fixed tree).  The grid is one
+// cluster, whose CTA 0 adds the CTAs' shares of the loss; Σ c·S is formed and
+// summed in binary64 (at most 1024 terms).
+constexpr int RT = 1024;
+
+__global__ void __launch_bounds__(RT) router_reduce_kernel(const float* part_p, const int* part_c,
+                                                           int P, int E, int k, int* counts,
+                                                           float* loss) {
+    __shared__ float2 ss[32][33];
+    __shared__ int sc[32][33];
+    __shared__ double all_share[8];
+    __shared__ long long all_chose[8];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const unsigned me = cluster_ctarank(), cs = cluster_nctarank();
+    double share = 0.0;
+    long long chose = 0;
+    for (int e0 = me * 32; e0 < E; e0 += cs * 32) {
+        const int e = e0 + lane;
+        Acc2 s = acc2_zero();
+        int c = 0;
+        for (int p0 = wid; p0 < P; p0 += 32 * 4) {
+            float v[4];
+            int n[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const bool in = e < E && p0 + 32 * i < P;
+                v[i] = in ? __ldg(part_p + (int64_t)(p0 + 32 * i) * E + e) : 0.f;
+                n[i] = in ? __ldg(part_c + (int64_t)(p0 + 32 * i) * E + e) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc2_add1(s, v[i]), c += n[i];
+        }
+        ss[wid][lane] = make_float2(s.hi, s.lo);
+        sc[wid][lane] = c;
+        __syncthreads();
+        for (int h = 16; h > 0; h >>= 1) {
+            if (wid < h) {
+                const float2 o = ss[wid + h][lane];
+                s = acc2_add(s, Acc2{o.x, o.y});
+                c += sc[wid + h][lane];
+                ss[wid][lane] = make_float2(s.hi, s.lo);
+                sc[wid][lane] = c;
+            }
+            __syncthreads();
+        }
+        if (wid == 0) {
+            if (e < E) counts[e] = c;
+            double t = (double)c * ((double)s.hi + (double)s.lo);
+            long long n = c;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                t += __shfl_xor_sync(FULL_MASK, t, o);
+                n += __shfl_xor_sync(FULL_MASK, n, o);
+            }
+            share += t;
+            chose += n;
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        const uint32_t ds = cluster_map(&all_share[me], 0), dc = cluster_map(&all_chose[me], 0);
+        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(ds), "d"(share) : "memory");
+        asm volatile("st.shared::cluster.s64 [%0], %1;" ::"r"(dc), "l"(chose) : "memory");
+    }
+    cluster_sync();
+    if (me == 0 && threadIdx.x == 0) {
+        share = 0.0, chose = 0;
+        for (unsigned r = 0; r < cs; r++) share += all_share[r], chose += all_chose[r];
+        // V = chose / k rows count: loss = E·Σ c·S / (k·V²) = E·k·Σ c·S / chose²
+        *loss = chose ? (float)((double)E * k * share / ((double)chose * (double)chose)) : 0.f;
+    }
+    pdl_trigger();
+}
+
+// ---------------------------------------------------------------------------
+struct BwdArgs {
+    const void* logits;
+    const int* ids;
+    const int* counts;
+    const float* dgates;
+    const float* dloss;
+    void* dlogits;
+    int64_t ld, ldd;
+    int64_t T;
+    int E, k, renorm, vec;
+};
 
 template <typename T, int L, int R>
 __device__ __forceinline__ void store_row(T* row, int sub, int E, bool vec,
@@ -145,223 +515,14 @@ __device__ __forceinline__ void store_row(T* row, int sub, int E, bool vec,
     }
 }
 
-// ---------------------------------------------------------------------------
-struct FwdArgs {
-    const void* logits;
-    const unsigned char* mask;
-    float* gates;
-    int* ids;
-    float* part_p;  // [P, E]
-    int* part_c;    // [P, E]
-    int64_t ld;
-    int64_t T;
-    int E, k, renorm, vec;
-};
-
-template <int L, int R>
-size_t fwd_smem(int k) {
-    return (size_t)(NW + 1) * L * 8 * R * 4 + (size_t)NW * (32 / L) * k * 8;
-}
-
-template <typename T, int L, int R>
-__global__ void __launch_bounds__(NT) router_fwd_kernel(const FwdArgs a) {
-    constexpr int EPL = 8 * R, RPW = 32 / L, SLOTS = L * EPL;
-    extern __shared__ float4 smem4[];
-    float* ps = reinterpret_cast<float*>(smem4);             // [NW][SLOTS]
-    int* cnt = reinterpret_cast<int*>(ps + NW * SLOTS);      // [SLOTS]
-    float2* took = reinterpret_cast<float2*>(cnt + SLOTS);   // [NW][RPW][k]: value, expert
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int sub = lane & (L - 1), grp = lane / L;
-    const int E = a.E, k = a.k;
-    float2* mine = took + (wid * RPW + grp) * k;
-
-    for (int i = threadIdx.x; i < SLOTS; i += NT) cnt[i] = 0;
-    __syncthreads();
-    pdl_wait();
-    float sum_p[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; i++) sum_p[i] = 0.f;
-
-    const int64_t step = (int64_t)gridDim.x * NW * RPW;
-    for (int64_t row0 = ((int64_t)blockIdx.x * NW + wid) * RPW; row0 < a.T; row0 += step) {
-        const int64_t row = row0 + grp;
-        const bool on = row < a.T;
-        float f[EPL];
-        load_row<T, L, R>((const T*)a.logits + row * a.ld, on, sub, E, a.vec, f);
-        bool valid = on && (!a.mask || a.mask[row]);
-
-        // the k largest, in order
-        uint32_t key[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            const int e = expert<L>(i, sub);
-            key[i] = e < E ? order_key<T>(f[i], e) : 0u;
-        }
-        float m = 0.f;
-        for (int j = 0; j < k; j++) {
-            uint32_t best = key[0];
-            int id;
-            if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int i = 1; i < EPL; i++) best = max(best, key[i]);
-                if constexpr (L == 32) {
-                    best = __reduce_max_sync(FULL_MASK, best);
-                } else {
-#pragma unroll
-                    for (int o = L / 2; o > 0; o >>= 1)
-                        best = max(best, __shfl_xor_sync(FULL_MASK, best, o));
-                }
-#pragma unroll
-                for (int i = 0; i < EPL; i++) key[i] = key[i] == best ? 0u : key[i];
-                id = 0xffff - (int)(best & 0xffffu);
-            } else {
-                id = expert<L>(0, sub);
-#pragma unroll
-                for (int i = 1; i < EPL; i++) {
-                    const bool up = key[i] > best;  // in index order: a tie keeps the first
-                    best = up ? key[i] : best;
-                    id = up ? expert<L>(i, sub) : id;
-                }
-#pragma unroll
-                for (int o = L / 2; o > 0; o >>= 1) {
-                    const uint32_t ob = __shfl_xor_sync(FULL_MASK, best, o);
-                    const int oi = __shfl_xor_sync(FULL_MASK, id, o);
-                    const bool up = ob > best || (ob == best && oi < id);
-                    best = up ? ob : best;
-                    id = up ? oi : id;
-                }
-#pragma unroll
-                for (int i = 0; i < EPL; i++)
-                    key[i] = expert<L>(i, sub) == id ? 0u : key[i];
-            }
-            const float v = key_value<T>(best);
-            if (j == 0) m = v;
-            if (sub == 0) mine[j] = make_float2(v, __int_as_float(id));
-        }
-        valid = valid && m != ninf();  // no logit above −inf: the row does not count
-
-        // softmax, shifted by the largest
-        m = valid ? m : 0.f;
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            f[i] = exp_of(f[i], m);
-            z += f[i];
-        }
-        z = group_sum<L>(z);
-        if (valid) {
-            const float inv = 1.0f / z;
-#pragma unroll
-            for (int i = 0; i < EPL; i++) sum_p[i] = fmaf(f[i], inv, sum_p[i]);
-        }
-
-        // gates and ids, in the order of memory
-        __syncwarp();
-        if (a.renorm) {
-            z = 0.f;
-            for (int j = sub; j < k; j += L) z += exp_of(mine[j].x, m);
-            z = group_sum<L>(z);
-        }
-        if (on) {
-            for (int j = sub; j < k; j += L) {
-                const float2 q = mine[j];
-                const int id = __float_as_int(q.y);
-                a.gates[row * k + j] = valid ? exp_of(q.x, m) / z : 0.f;
-                a.ids[row * k + j] = valid ? id : -1;
-                if (valid) atomicAdd(&cnt[id], 1);
-            }
-        }
-        __syncwarp();
-    }
-
-    // the block's sums: over the warp's rows, then over the warps in order
-#pragma unroll
-    for (int i = 0; i < EPL; i++) {
-        float v = sum_p[i];
-#pragma unroll
-        for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
-        if (grp == 0) ps[wid * SLOTS + expert<L>(i, sub)] = v;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += NT) {
-        float v = ps[e];
-#pragma unroll
-        for (int w = 1; w < NW; w++) v += ps[w * SLOTS + e];
-        a.part_p[(int64_t)blockIdx.x * E + e] = v;
-        a.part_c[(int64_t)blockIdx.x * E + e] = cnt[e];
-    }
-    pdl_trigger();
-}
-
-// counts, and the loss, from the P partial rows: column e is summed by 32
-// threads (rows p ≡ stripe mod 32 in order, then a fixed butterfly).  The
-// grid is one cluster; CTA 0 adds the CTAs' shares of the loss.  c·S is
-// formed and summed in binary64: at most 1024 terms.
-constexpr int RT = 1024;
-
-__global__ void __launch_bounds__(RT) router_reduce_kernel(const float* part_p, const int* part_c,
-                                                           int P, int E, int k, int* counts,
-                                                           float* loss) {
-    __shared__ double share[RT / 32];
-    __shared__ long long chose[RT / 32];
-    __shared__ double all_share[8];
-    __shared__ long long all_chose[8];
-    pdl_wait();
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const unsigned me = cluster_ctarank(), cs = cluster_nctarank();
-    double sh = 0.0;
-    long long ch = 0;
-    for (int e = me * (RT / 32) + wid; e < E; e += cs * (RT / 32)) {
-        Acc2 s = acc2_zero();
-        int c = 0;
-        for (int p = lane; p < P; p += 32) {
-            acc2_add1(s, __ldg(part_p + (int64_t)p * E + e));
-            c += __ldg(part_c + (int64_t)p * E + e);
-        }
-        s = group_sum2<32>(s);
-        c = __reduce_add_sync(FULL_MASK, c);
-        if (lane == 0) counts[e] = c;
-        sh += (double)c * ((double)s.hi + (double)s.lo);
-        ch += c;
-    }
-    if (lane == 0) share[wid] = sh, chose[wid] = ch;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < RT / 32; w++) sh += share[w], ch += chose[w];
-        const uint32_t ds = cluster_map(&all_share[me], 0), dc = cluster_map(&all_chose[me], 0);
-        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(ds), "d"(sh) : "memory");
-        asm volatile("st.shared::cluster.s64 [%0], %1;" ::"r"(dc), "l"(ch) : "memory");
-    }
-    cluster_sync();
-    if (me == 0 && threadIdx.x == 0) {
-        sh = 0.0, ch = 0;
-        for (unsigned r = 0; r < cs; r++) sh += all_share[r], ch += all_chose[r];
-        // V = ch / k rows count: loss = E·Σ c·S / (k·V²) = E·k·Σ c·S / ch²
-        *loss = ch ? (float)((double)E * k * sh / ((double)ch * (double)ch)) : 0.f;
-    }
-    pdl_trigger();
-}
-
-// ---------------------------------------------------------------------------
-struct BwdArgs {
-    const void* logits;
-    const int* ids;
-    const int* counts;
-    const float* dgates;
-    const float* dloss;
-    void* dlogits;
-    int64_t ld, ldd;
-    int64_t T;
-    int E, k, renorm, vec;
-};
-
 template <int L, int R>
 size_t bwd_smem() {
     return (size_t)NW * 32 * 8 * R * 4 + 64;
 }
 
 template <typename T, int L, int R>
-__global__ void __launch_bounds__(NT) router_bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
+    router_bwd_kernel(const BwdArgs a) {
     constexpr int EPL = 8 * R, RPW = 32 / L, SLOTS = L * EPL;
     extern __shared__ float4 smem4[];
     float* put = reinterpret_cast<float*>(smem4);  // [NW][RPW][SLOTS]: gradients at their experts
@@ -384,104 +545,156 @@ __global__ void __launch_bounds__(NT) router_bwd_kernel(const BwdArgs a) {
     // a_e = dloss·E·c_e/(k·V²) = dloss·E·k·c_e/ch²
     const float V = (float)ch / k;
     const float unit = ch > 0 && a.dloss ? *a.dloss * ((float)E / (k * V)) / V : 0.f;
-    float ae[EPL];
+    uint64_t ae[EPL / 2];
 #pragma unroll
-    for (int i = 0; i < EPL; i++) {
+    for (int i = 0; i < EPL; i += 2) {
         const int e = expert<L>(i, sub);
-        ae[i] = e < E ? unit * (float)a.counts[e] : 0.f;
+        ae[i / 2] = f2_pack(e < E ? unit * (float)a.counts[e] : 0.f,
+                            e + 1 < E ? unit * (float)a.counts[e + 1] : 0.f);
     }
 
     const int64_t step = (int64_t)gridDim.x * NW * RPW;
-    for (int64_t row0 = ((int64_t)blockIdx.x * NW + wid) * RPW; row0 < a.T; row0 += step) {
-        const int64_t row = row0 + grp;
+    int64_t row = ((int64_t)blockIdx.x * NW + wid) * RPW + grp;
+    // a row, and the lane's first choice of it (most rows have one a lane at
+    // most), a turn ahead
+    Logits<T, L, R> next;
+    int next_id = -1;
+    float next_dg = 0.f;
+    auto ask = [&](int64_t r) {
+        next.load((const T*)a.logits + r * a.ld, r < a.T, sub, E, a.vec);
+        next_id = -1;
+        if (r < a.T && sub < k) {
+            next_id = __ldg(a.ids + r * k + sub);
+            if (a.dgates) next_dg = __ldg(a.dgates + r * k + sub);
+        }
+    };
+    ask(row);
+    for (; row - grp < a.T; row += step) {
+        const Logits<T, L, R> x = next;
+        const int id0 = next_id;
+        const float dg0 = next_dg;
+        ask(row + step);
         const bool on = row < a.T;
         const T* src = (const T*)a.logits + row * a.ld;
-        float f[EPL];
-        load_row<T, L, R>(src, on, sub, E, a.vec, f);
         const int* ids = a.ids + row * k;
-        const bool valid = on && ids[0] >= 0;
-        float m = f[0];
+        const bool valid = __shfl_sync(FULL_MASK, id0, lane & ~(L - 1)) >= 0;
+        const bool put_u = valid && a.dgates;
+
+        uint64_t f[EPL / 2];
+        x.widen(f);
+        float m = ninf();
 #pragma unroll
-        for (int i = 1; i < EPL; i++) m = fmaxf(m, f[i]);
+        for (int i = 0; i < EPL / 2; i++) {
+            float p, q;
+            f2_unpack(f[i], p, q);
+            m = fmaxf(m, fmaxf(p, q));
+        }
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
         m = valid ? m : 0.f;
 
         // the gates' gradient, at its experts
-        const bool put_u = valid && a.dgates;
+        float zs = 0.f, ds = 0.f;
         if (a.renorm) {
-            float zs = 0.f, dot = 0.f;
-            if (put_u)
+            if (put_u) {
                 for (int j = sub; j < k; j += L) {
-                    const unsigned id = ids[j];
+                    const unsigned id = j == sub ? id0 : ids[j];
                     if (id >= (unsigned)E) continue;
                     const float e = exp_of(Elt<T>::load1(src + id), m);
                     zs += e;
-                    dot = fmaf(e, a.dgates[row * k + j], dot);
+                    ds = fmaf(e, j == sub ? dg0 : a.dgates[row * k + j], ds);
                 }
+            }
             zs = group_sum<L>(zs);
-            dot = group_sum<L>(dot) / zs;
-            if (put_u)
-                for (int j = sub; j < k; j += L) {
-                    const unsigned id = ids[j];
-                    if (id >= (unsigned)E) continue;
-                    const float e = exp_of(Elt<T>::load1(src + id), m);
-                    mine[id] = e / zs * (a.dgates[row * k + j] - dot);
-                }
-        } else if (put_u) {
+            ds = group_sum<L>(ds) / zs;
+        }
+        if (put_u) {
             for (int j = sub; j < k; j += L) {
-                const unsigned id = ids[j];
-                if (id < (unsigned)E) mine[id] = a.dgates[row * k + j];
+                const unsigned id = j == sub ? id0 : ids[j];
+                if (id >= (unsigned)E) continue;
+                float u = j == sub ? dg0 : a.dgates[row * k + j];
+                if (a.renorm) u = exp_of(Elt<T>::load1(src + id), m) / zs * (u - ds);
+                mine[id] = u;
             }
         }
         __syncwarp();
-        float u[EPL];
+        uint64_t u[EPL / 2];
 #pragma unroll
         for (int i = 0; i < EPL; i += 4) {
             const float4 q = *reinterpret_cast<const float4*>(mine + expert<L>(i, sub));
-            u[i] = q.x, u[i + 1] = q.y, u[i + 2] = q.z, u[i + 3] = q.w;
+            u[i / 2] = f2_pack(q.x, q.y);
+            u[i / 2 + 1] = f2_pack(q.z, q.w);
         }
         __syncwarp();
         if (put_u)
-            for (int j = sub; j < k; j += L)
-                if ((unsigned)ids[j] < (unsigned)E) mine[ids[j]] = 0.f;
+            for (int j = sub; j < k; j += L) {
+                const unsigned id = j == sub ? id0 : ids[j];
+                if (id < (unsigned)E) mine[id] = 0.f;
+            }
 
-        float z = 0.f, dot = 0.f;
+        const uint64_t m2 = f2_pack(m, m), l2 = f2_pack(kLog2e, kLog2e);
+        uint64_t z2 = f2_pack(0.f, 0.f), d2 = z2;
+        // plain gates: g = a + u; normalised: g = a, and u is added at the end
+        uint64_t g[EPL / 2];
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            f[i] = exp_of(f[i], m);
-            z += f[i];
-            dot = fmaf(f[i], a.renorm ? ae[i] : ae[i] + u[i], dot);
+        for (int i = 0; i < EPL / 2; i++) {
+            float p, q;
+            f2_unpack(f2_mul(f2_sub(f[i], m2), l2), p, q);
+            f[i] = f2_pack(ex2(p), ex2(q));
+            z2 = f2_add(z2, f[i]);
+            g[i] = a.renorm ? ae[i] : f2_add(ae[i], u[i]);
+            if (!a.renorm) u[i] = f2_pack(0.f, 0.f);
+            d2 = f2_fma(f[i], g[i], d2);
         }
-        z = group_sum<L>(z);
-        dot = group_sum<L>(dot) / z;
+        float z, dot, z1, dot1;
+        f2_unpack(z2, z, z1);
+        f2_unpack(d2, dot, dot1);
+        z += z1;
+        dot += dot1;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) {
+            z1 = __shfl_xor_sync(FULL_MASK, z, o);
+            dot1 = __shfl_xor_sync(FULL_MASK, dot, o);
+            z += z1;
+            dot += dot1;
+        }
         const float inv = 1.0f / z;
+        dot *= inv;
+        const uint64_t i2 = f2_pack(inv, inv), n2 = f2_pack(dot, dot);
+        float out[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            const float p = f[i] * inv;
-            f[i] = a.renorm ? fmaf(p, ae[i] - dot, u[i]) : p * (ae[i] + u[i] - dot);
-            if (!valid) f[i] = 0.f;
+        for (int i = 0; i < EPL / 2; i++) {
+            const uint64_t v = f2_fma(f2_mul(f[i], i2), f2_sub(g[i], n2), u[i]);
+            f2_unpack(v, out[2 * i], out[2 * i + 1]);
+            if (!valid) out[2 * i] = out[2 * i + 1] = 0.f;
         }
-        if (on) store_row<T, L, R>((T*)a.dlogits + row * a.ldd, sub, E, a.vec, f);
+        if (on) store_row<T, L, R>((T*)a.dlogits + row * a.ldd, sub, E, a.vec, out);
         __syncwarp();
     }
     pdl_trigger();
 }
 
-// Blocks of the forward (rows of the partial sums) and of the backward: at
-// most four an SM, each with two turns of its warps or more.
-int64_t blocks_for(int64_t T, int64_t E) {
+// Blocks of the forward (rows of the partial sums) and of the backward: as
+// many as the SMs hold at once, each with two turns of its warps or more.
+int64_t blocks_for(int64_t T, int64_t E, bool backward) {
     int L = 1;
     while (L < 32 && L * 8 < E) L *= 2;
     const int64_t rows = (int64_t)NW * (32 / L) * 2;
+    const int64_t most = kDesignSMs * (E > 512 ? 1 : E > 256 ? 2 : backward ? 3 : 4);
     const int64_t b = (T + rows - 1) / rows;
-    return b < 1 ? 1 : b > kDesignSMs * 4 ? kDesignSMs * 4 : b;
+    return b < 1 ? 1 : b > most ? most : b;
 }
 
 template <typename T, int L, int R>
 cudaError_t run_fwd(const FwdArgs& a, int64_t P, cudaStream_t s) {
-    return launch(router_fwd_kernel<T, L, R>, dim3((unsigned)P), dim3(NT), fwd_smem<L, R>(a.k), s,
-                  true, a);
+    const size_t smem = fwd_smem<T, L, R>(a.k);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute((const void*)router_fwd_kernel<T, L, R>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(router_fwd_kernel<T, L, R>, dim3((unsigned)P), dim3(NT), smem, s, true, a);
 }
 template <typename T, int L, int R>
 cudaError_t run_bwd(const BwdArgs& a, int64_t P, cudaStream_t s) {
@@ -506,7 +719,7 @@ bool vectors(const void* p, int64_t ld, int E, int es, int64_t T) {
 
 }  // namespace
 
-int64_t router_tiles(int64_t T, int64_t E) { return T > 0 ? blocks_for(T, E) : 0; }
+int64_t router_tiles(int64_t T, int64_t E) { return T > 0 ? blocks_for(T, E, false) : 0; }
 
 cudaError_t launch_router_fwd(const void* logits, int64_t ld, const unsigned char* mask, int64_t k,
                               int renorm, float* gates, int* ids, int* counts, float* loss,
@@ -531,8 +744,8 @@ cudaError_t launch_router_bwd(const void* logits, int64_t ld, const int* ids, co
                               int64_t k, int renorm, const float* dgates, const float* dloss,
                               void* dlogits, int64_t ldd, int64_t T, int64_t E, int dtype,
                               cudaStream_t s) {
-    const int64_t P = router_tiles(T, E);
-    if (P == 0) return cudaSuccess;
+    if (T == 0) return cudaSuccess;
+    const int64_t P = blocks_for(T, E, true);
     const int es = elt_bytes(dtype);
     const BwdArgs a{logits, ids, counts, dgates, dloss, dlogits, ld, ldd, T, (int)E, (int)k, renorm,
                     vectors(logits, ld, (int)E, es, T) && vectors(dlogits, ldd, (int)E, es, T)};
