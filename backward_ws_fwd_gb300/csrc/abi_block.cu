@@ -236,7 +236,8 @@ int rotary_bwd(const void* dyq, const int64_t* dyq_strides, void* dq, const int6
 
 size_t router_fwd_workspace_bytes(int64_t T, int64_t E) {
     if (T < 0 || E < 1 || E > wsf::kRouterMaxE) return SIZE_MAX;
-    return (size_t)(wsf::router_tiles(T, E) * E * 8);
+    const int64_t P = wsf::router_tiles(T, E);  // one block joins its sums itself
+    return P > 1 ? (size_t)(P * E * 8) : 0;
 }
 
 int router_fwd(const void* logits, int64_t ld, const unsigned char* mask, int64_t k,

@@ -50,6 +50,28 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// 1/x by the hardware's reciprocal (1 unit in the last place; the sums it is
+// taken of lie between 1 and the number of experts).
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Maximum over a row's lanes.
+template <int L>
+__device__ __forceinline__ float row_max(float v) {
+    if constexpr (L == 32) {
+        float m;
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+        return m;
+    } else {
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL_MASK, v, o));
+        return v;
+    }
+}
+
 // exp(f − m).  The difference is taken first: m·log₂ e alone overflows where
 // every logit is the type's lowest value.
 __device__ __forceinline__ float exp_of(float f, float m) { return ex2((f - m) * kLog2e); }
@@ -69,37 +91,46 @@ struct Logits {
     static constexpr int W = 8 * (int)sizeof(T) / 4;  // words of a run
     uint32_t w[R * W];
 
-    __device__ __forceinline__ void load(const T* row, bool on, int sub, int E, bool vec) {
-        const uint32_t none = sizeof(T) == 4                     ? 0xff800000u
-                              : std::is_same<T, __half>::value ? 0xfc00fc00u
-                                                               : 0xff80ff80u;
+    // What lies behind the last expert is put right by end(), when the row's
+    // turn comes: touching the words here would wait for the load.
+    __device__ __forceinline__ void load(const T* row, int sub, int E, bool vec) {
+        if (vec) {
 #pragma unroll
-        for (int i = 0; i < R * W; i++) w[i] = none;
-        if (!on) return;
+            for (int r = 0; r < R; r++) {
+                const int e0 = expert<L>(r * 8, sub), at = e0 < E ? e0 : 0;
 #pragma unroll
-        for (int r = 0; r < R; r++) {
-            const int e0 = expert<L>(r * 8, sub);
-            if (vec) {
-                if (e0 < E) {
+                for (int h = 0; h < W / 4; h++) {
+                    const Raw16 q = ld_keep(row + at + h * Elt<T>::V);
 #pragma unroll
-                    for (int h = 0; h < W / 4; h++) {
-                        const Raw16 q = ld_keep(row + e0 + h * Elt<T>::V);
-#pragma unroll
-                        for (int i = 0; i < 4; i++) w[r * W + h * 4 + i] = q.u[i];
-                    }
+                    for (int i = 0; i < 4; i++) w[r * W + h * 4 + i] = q.u[i];
                 }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8 * R; i++) {
+                const int e = min(expert<L>(i, sub), E - 1);
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = __ldg(reinterpret_cast<const uint32_t*>(row) + e);
+                } else {
+                    const uint32_t v = __ldg(reinterpret_cast<const unsigned short*>(row) + e);
+                    w[i / 2] = i & 1 ? w[i / 2] | v << 16 : v;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void end(int sub, int E) {
+        if (E == 8 * R * L) return;
+        constexpr uint32_t none = sizeof(T) == 4                     ? 0xff800000u
+                                  : std::is_same<T, __half>::value ? 0xfc00u
+                                                                   : 0xff80u;
+#pragma unroll
+        for (int i = 0; i < 8 * R; i++) {
+            const bool past = expert<L>(i, sub) >= E;
+            if constexpr (sizeof(T) == 4) {
+                w[i] = past ? none : w[i];
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    if (e0 + i >= E) continue;
-                    if constexpr (sizeof(T) == 4) {
-                        w[r * W + i] = __ldg(reinterpret_cast<const uint32_t*>(row) + e0 + i);
-                    } else {
-                        const uint32_t v = __ldg(reinterpret_cast<const unsigned short*>(row) + e0 + i);
-                        uint32_t& d = w[r * W + i / 2];
-                        d = i & 1 ? (d & 0xffffu) | v << 16 : (d & 0xffff0000u) | v;
-                    }
-                }
+                uint32_t& d = w[i / 2];
+                d = past ? (i & 1 ? (d & 0xffffu) | none << 16 : (d & 0xffff0000u) | none) : d;
             }
         }
     }
@@ -251,16 +282,24 @@ struct FwdArgs {
     int* ids;
     float* part_p;  // [P, E]
     int* part_c;    // [P, E]
+    int* counts;
+    float* loss;
     int64_t ld;
-    int64_t T;
+    int T;
     int E, k, renorm, vec;
 };
 
-// Shared memory: the sorted runs of every lane ([warp][run][place][lane]), the
-// chosen of every row, the counts; the warps' sums take the runs' place.
+// E·Σ c·S / (k·V²) with V = chose / k rows that count.
+__device__ __forceinline__ float balance(int E, int k, double share, long long chose) {
+    return chose ? (float)((double)E * k * share / ((double)chose * (double)chose)) : 0.f;
+}
+
+// Shared memory: the sorted runs of every lane ([warp][run][place][lane], nine
+// places, the last an end mark), the chosen of every row, the counts; the
+// warps' sums take the runs' place.
 template <typename T, int L, int R>
 size_t fwd_smem(int k) {
-    return (size_t)NT * 8 * R * sizeof(Pick<T>) + (size_t)NW * (32 / L) * k * sizeof(Pick<T>) +
+    return (size_t)NT * 9 * R * sizeof(Pick<T>) + (size_t)NW * (32 / L) * k * sizeof(Pick<T>) +
            (size_t)L * 8 * R * 4;
 }
 
@@ -271,33 +310,39 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
     constexpr int EPL = 8 * R, RPW = 32 / L, SLOTS = L * EPL;
     extern __shared__ float4 smem4[];
     P* runs = reinterpret_cast<P*>(smem4);
-    P* took = runs + NT * EPL;
+    P* took = runs + NT * 9 * R;
     int* cnt = reinterpret_cast<int*>(took + NW * RPW * a.k);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int sub = lane & (L - 1), grp = lane / L;
-    const int E = a.E, k = a.k;
-    P* run = runs + wid * 32 * EPL + lane;  // place q of run r: run[(r·8 + q)·32]
+    const int E = a.E, k = a.k, T_ = a.T;
+    P* run = runs + wid * 32 * 9 * R + lane;  // place q of run r: run[(r·9 + q)·32]
     P* mine = took + (wid * RPW + grp) * k;
 
     for (int i = threadIdx.x; i < SLOTS; i += NT) cnt[i] = 0;
+#pragma unroll
+    for (int r = 0; r < R; r++) run[(r * 9 + 8) * 32] = P::of(0u, -1);
     __syncthreads();
     pdl_wait();
     uint64_t sum_p[EPL / 2];
 #pragma unroll
     for (int i = 0; i < EPL / 2; i++) sum_p[i] = f2_pack(0.f, 0.f);
 
-    const int64_t step = (int64_t)gridDim.x * NW * RPW;
-    int64_t row = ((int64_t)blockIdx.x * NW + wid) * RPW + grp;
+    // (rows fit an int: T·k < 2³¹; rows behind the last read the last one)
+    const int step = gridDim.x * NW * RPW;
     Logits<T, L, R> next;
-    next.load((const T*)a.logits + row * a.ld, row < a.T, sub, E, a.vec);
-    bool keep = row < a.T && (!a.mask || a.mask[row]);
-    for (; row - grp < a.T; row += step) {
-        const Logits<T, L, R> x = next;
-        const bool on = row < a.T;
-        bool valid = keep;
-        // the next row is in flight meanwhile
-        next.load((const T*)a.logits + (row + step) * a.ld, row + step < a.T, sub, E, a.vec);
-        keep = row + step < a.T && (!a.mask || a.mask[row + step]);
+    unsigned char keep = 1;
+    auto ask = [&](int64_t r) {
+        const int64_t q = r < T_ ? r : T_ - 1;
+        next.load((const T*)a.logits + q * a.ld, sub, E, a.vec);
+        if (a.mask) keep = __ldg(a.mask + q);
+    };
+    int64_t row = (int)(blockIdx.x * NW + wid) * RPW + grp;
+    if (row - grp < T_) ask(row);
+    for (; row - grp < T_; row += step) {
+        Logits<T, L, R> x = next;
+        x.end(sub, E);
+        bool valid = keep && row < T_;
+        if (row - grp + step < T_) ask(row + step);  // in flight meanwhile
 
         // the k largest, in order: every lane sorts its runs and offers the
         // first of what is left of them
@@ -311,14 +356,12 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
             for (int q = 0; q < 8; q++) s[q] = P::of(key[r * 8 + q], expert<L>(r * 8 + q, sub));
             sort8(s);
             head[r] = s[0];
-            if (k > 1) {
 #pragma unroll
-                for (int q = 1; q < 8; q++) run[(r * 8 + q) * 32] = s[q];
-            }
+            for (int q = 1; q < 8; q++) run[(r * 9 + q) * 32] = s[q];
         }
-        int at[R];
+        P* at[R];  // the heads' places
 #pragma unroll
-        for (int r = 0; r < R; r++) at[r] = r * 256;  // the head's place, times 32
+        for (int r = 0; r < R; r++) at[r] = run + r * 9 * 32;
         float m = 0.f;
         for (int j = 0; j < k; j++) {
             P b = head[0];
@@ -330,11 +373,9 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
             if (sub == 0) mine[j] = b;
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                if (head[r].same(b)) {
-                    at[r] += 32;
-                    head[r] = P::of(0u, -1);
-                    if (at[r] < (r + 1) * 256) head[r] = run[at[r]];
-                }
+                const bool won = head[r].same(b);
+                at[r] += won ? 32 : 0;
+                if (won) head[r] = *at[r];
             }
         }
         valid = valid && m != ninf();  // no logit above −inf: the row does not count
@@ -355,8 +396,8 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
         float z, z1;
         f2_unpack(z2, z, z1);
         z = group_sum<L>(z + z1);
+        float inv = rcp(z);
         if (valid) {
-            const float inv = 1.0f / z;
             const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
             for (int i = 0; i < EPL / 2; i++) sum_p[i] = f2_fma(f[i], inv2, sum_p[i]);
@@ -367,13 +408,14 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
         if (a.renorm) {
             z = 0.f;
             for (int j = sub; j < k; j += L) z += exp_of(key_value<T>(mine[j].key), m);
-            z = group_sum<L>(z);
+            inv = rcp(group_sum<L>(z));
         }
-        if (on) {
+        if (row < T_) {
             for (int j = sub; j < k; j += L) {
                 const P q = mine[j];
-                a.gates[row * k + j] = valid ? exp_of(key_value<T>(q.key), m) / z : 0.f;
-                a.ids[row * k + j] = valid ? q.id() : -1;
+                const int to = (int)row * k + j;
+                a.gates[to] = valid ? exp_of(key_value<T>(q.key), m) * inv : 0.f;
+                a.ids[to] = valid ? q.id() : -1;
                 if (valid) atomicAdd(&cnt[q.id()], 1);
             }
         }
@@ -393,12 +435,35 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
         if (grp == 0) ps[wid * SLOTS + expert<L>(i, sub)] = u;
     }
     __syncthreads();
+    double share = 0.0;
+    long long chose = 0;
     for (int e = threadIdx.x; e < E; e += NT) {
         float v = ps[e];
 #pragma unroll
         for (int w = 1; w < NW; w++) v += ps[w * SLOTS + e];
-        a.part_p[(int64_t)blockIdx.x * E + e] = v;
-        a.part_c[(int64_t)blockIdx.x * E + e] = cnt[e];
+        if (gridDim.x > 1) {
+            a.part_p[(int64_t)blockIdx.x * E + e] = v;
+            a.part_c[(int64_t)blockIdx.x * E + e] = cnt[e];
+        } else {  // few rows: this block has all of them
+            a.counts[e] = cnt[e];
+            share += (double)cnt[e] * v;
+            chose += cnt[e];
+        }
+    }
+    if (gridDim.x == 1) {
+        __shared__ double all_share[NW];
+        __shared__ long long all_chose[NW];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            share += __shfl_xor_sync(FULL_MASK, share, o);
+            chose += __shfl_xor_sync(FULL_MASK, chose, o);
+        }
+        if (lane == 0) all_share[wid] = share, all_chose[wid] = chose;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < NW; w++) share += all_share[w], chose += all_chose[w];
+            *a.loss = balance(E, k, share, chose);
+        }
     }
     pdl_trigger();
 }
@@ -425,17 +490,17 @@ __global__ void __launch_bounds__(RT) router_reduce_kernel(const float* part_p, 
         const int e = e0 + lane;
         Acc2 s = acc2_zero();
         int c = 0;
-        for (int p0 = wid; p0 < P; p0 += 32 * 4) {
-            float v[4];
-            int n[4];
+        for (int p0 = wid; p0 < P; p0 += 32 * 8) {
+            float v[8];
+            int n[8];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < 8; i++) {
                 const bool in = e < E && p0 + 32 * i < P;
                 v[i] = in ? __ldg(part_p + (int64_t)(p0 + 32 * i) * E + e) : 0.f;
                 n[i] = in ? __ldg(part_c + (int64_t)(p0 + 32 * i) * E + e) : 0;
             }
 #pragma unroll
-            for (int i = 0; i < 4; i++) acc2_add1(s, v[i]), c += n[i];
+            for (int i = 0; i < 8; i++) acc2_add1(s, v[i]), c += n[i];
         }
         ss[wid][lane] = make_float2(s.hi, s.lo);
         sc[wid][lane] = c;
@@ -473,8 +538,7 @@ __global__ void __launch_bounds__(RT) router_reduce_kernel(const float* part_p, 
     if (me == 0 && threadIdx.x == 0) {
         share = 0.0, chose = 0;
         for (unsigned r = 0; r < cs; r++) share += all_share[r], chose += all_chose[r];
-        // V = chose / k rows count: loss = E·Σ c·S / (k·V²) = E·k·Σ c·S / chose²
-        *loss = chose ? (float)((double)E * k * share / ((double)chose * (double)chose)) : 0.f;
+        *loss = balance(E, k, share, chose);
     }
     pdl_trigger();
 }
@@ -488,7 +552,7 @@ struct BwdArgs {
     const float* dloss;
     void* dlogits;
     int64_t ld, ldd;
-    int64_t T;
+    int T;
     int E, k, renorm, vec;
 };
 
@@ -520,7 +584,7 @@ size_t bwd_smem() {
     return (size_t)NW * 32 * 8 * R * 4 + 64;
 }
 
-template <typename T, int L, int R>
+template <typename T, int L, int R, bool Renorm>
 __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
     router_bwd_kernel(const BwdArgs a) {
     constexpr int EPL = 8 * R, RPW = 32 / L, SLOTS = L * EPL;
@@ -553,32 +617,34 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
                             e + 1 < E ? unit * (float)a.counts[e + 1] : 0.f);
     }
 
-    const int64_t step = (int64_t)gridDim.x * NW * RPW;
-    int64_t row = ((int64_t)blockIdx.x * NW + wid) * RPW + grp;
-    // a row, and the lane's first choice of it (most rows have one a lane at
-    // most), a turn ahead
+    const int step = gridDim.x * NW * RPW, T_ = a.T;
+    const bool few = k <= L;  // one choice a lane
+    // a row, and the lane's first choice of it, a turn ahead
     Logits<T, L, R> next;
     int next_id = -1;
     float next_dg = 0.f;
     auto ask = [&](int64_t r) {
-        next.load((const T*)a.logits + r * a.ld, r < a.T, sub, E, a.vec);
+        const int64_t q = r < T_ ? r : T_ - 1;
+        next.load((const T*)a.logits + q * a.ld, sub, E, a.vec);
         next_id = -1;
-        if (r < a.T && sub < k) {
-            next_id = __ldg(a.ids + r * k + sub);
-            if (a.dgates) next_dg = __ldg(a.dgates + r * k + sub);
+        if (r < T_ && sub < k) {
+            next_id = __ldg(a.ids + q * k + sub);
+            if (a.dgates) next_dg = __ldg(a.dgates + q * k + sub);
         }
     };
-    ask(row);
-    for (; row - grp < a.T; row += step) {
-        const Logits<T, L, R> x = next;
+    int64_t row = (int)(blockIdx.x * NW + wid) * RPW + grp;
+    if (row - grp < T_) ask(row);
+    for (; row - grp < T_; row += step) {
+        Logits<T, L, R> x = next;
+        x.end(sub, E);
         const int id0 = next_id;
         const float dg0 = next_dg;
-        ask(row + step);
-        const bool on = row < a.T;
+        if (row - grp + step < T_) ask(row + step);
         const T* src = (const T*)a.logits + row * a.ld;
         const int* ids = a.ids + row * k;
+        const float* dg = a.dgates + row * k;
         const bool valid = __shfl_sync(FULL_MASK, id0, lane & ~(L - 1)) >= 0;
-        const bool put_u = valid && a.dgates;
+        const bool put_u = valid && a.dgates, put0 = put_u && (unsigned)id0 < (unsigned)E;
 
         uint64_t f[EPL / 2];
         x.widen(f);
@@ -589,31 +655,36 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
             f2_unpack(f[i], p, q);
             m = fmaxf(m, fmaxf(p, q));
         }
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL_MASK, m, o));
+        m = row_max<L>(m);
         m = valid ? m : 0.f;
 
         // the gates' gradient, at its experts
-        float zs = 0.f, ds = 0.f;
-        if (a.renorm) {
-            if (put_u) {
-                for (int j = sub; j < k; j += L) {
-                    const unsigned id = j == sub ? id0 : ids[j];
+        float u0 = dg0, zs = 0.f, ds = 0.f;
+        if constexpr (Renorm) {
+            float e0 = 0.f;
+            if (put0) e0 = exp_of(Elt<T>::load1(src + id0), m);
+            zs = e0;
+            ds = e0 * dg0;
+            if (!few && put_u) {
+                for (int j = sub + L; j < k; j += L) {
+                    const unsigned id = ids[j];
                     if (id >= (unsigned)E) continue;
                     const float e = exp_of(Elt<T>::load1(src + id), m);
                     zs += e;
-                    ds = fmaf(e, j == sub ? dg0 : a.dgates[row * k + j], ds);
+                    ds = fmaf(e, dg[j], ds);
                 }
             }
-            zs = group_sum<L>(zs);
-            ds = group_sum<L>(ds) / zs;
+            zs = rcp(group_sum<L>(zs));
+            ds = group_sum<L>(ds) * zs;
+            u0 = e0 * zs * (dg0 - ds);
         }
-        if (put_u) {
-            for (int j = sub; j < k; j += L) {
-                const unsigned id = j == sub ? id0 : ids[j];
+        if (put0) mine[id0] = u0;
+        if (!few && put_u) {
+            for (int j = sub + L; j < k; j += L) {
+                const unsigned id = ids[j];
                 if (id >= (unsigned)E) continue;
-                float u = j == sub ? dg0 : a.dgates[row * k + j];
-                if (a.renorm) u = exp_of(Elt<T>::load1(src + id), m) / zs * (u - ds);
+                float u = dg[j];
+                if constexpr (Renorm) u = exp_of(Elt<T>::load1(src + id), m) * zs * (u - ds);
                 mine[id] = u;
             }
         }
@@ -626,25 +697,22 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
             u[i / 2 + 1] = f2_pack(q.z, q.w);
         }
         __syncwarp();
-        if (put_u)
-            for (int j = sub; j < k; j += L) {
-                const unsigned id = j == sub ? id0 : ids[j];
-                if (id < (unsigned)E) mine[id] = 0.f;
-            }
+        if (put0) mine[id0] = 0.f;
+        if (!few && put_u)
+            for (int j = sub + L; j < k; j += L)
+                if ((unsigned)ids[j] < (unsigned)E) mine[ids[j]] = 0.f;
 
+        // plain gates: g = a + u; normalised: g = a, and u is added at the end
         const uint64_t m2 = f2_pack(m, m), l2 = f2_pack(kLog2e, kLog2e);
         uint64_t z2 = f2_pack(0.f, 0.f), d2 = z2;
-        // plain gates: g = a + u; normalised: g = a, and u is added at the end
-        uint64_t g[EPL / 2];
 #pragma unroll
         for (int i = 0; i < EPL / 2; i++) {
             float p, q;
             f2_unpack(f2_mul(f2_sub(f[i], m2), l2), p, q);
             f[i] = f2_pack(ex2(p), ex2(q));
             z2 = f2_add(z2, f[i]);
-            g[i] = a.renorm ? ae[i] : f2_add(ae[i], u[i]);
-            if (!a.renorm) u[i] = f2_pack(0.f, 0.f);
-            d2 = f2_fma(f[i], g[i], d2);
+            if constexpr (!Renorm) u[i] = f2_add(ae[i], u[i]);
+            d2 = f2_fma(f[i], Renorm ? ae[i] : u[i], d2);
         }
         float z, dot, z1, dot1;
         f2_unpack(z2, z, z1);
@@ -658,30 +726,37 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
             z += z1;
             dot += dot1;
         }
-        const float inv = 1.0f / z;
+        const float inv = rcp(z);
         dot *= inv;
         const uint64_t i2 = f2_pack(inv, inv), n2 = f2_pack(dot, dot);
         float out[EPL];
 #pragma unroll
         for (int i = 0; i < EPL / 2; i++) {
-            const uint64_t v = f2_fma(f2_mul(f[i], i2), f2_sub(g[i], n2), u[i]);
+            const uint64_t p = f2_mul(f[i], i2);
+            const uint64_t v = Renorm ? f2_fma(p, f2_sub(ae[i], n2), u[i])
+                                      : f2_mul(p, f2_sub(u[i], n2));
             f2_unpack(v, out[2 * i], out[2 * i + 1]);
-            if (!valid) out[2 * i] = out[2 * i + 1] = 0.f;
         }
-        if (on) store_row<T, L, R>((T*)a.dlogits + row * a.ldd, sub, E, a.vec, out);
+        if (!valid) {
+#pragma unroll
+            for (int i = 0; i < EPL; i++) out[i] = 0.f;
+        }
+        if (row < T_) store_row<T, L, R>((T*)a.dlogits + row * a.ldd, sub, E, a.vec, out);
         __syncwarp();
     }
     pdl_trigger();
 }
 
 // Blocks of the forward (rows of the partial sums) and of the backward: as
-// many as the SMs hold at once, each with two turns of its warps or more.
+// many as the SMs hold at once, each with two turns of its warps or more.  Up
+// to four turns of one block stay in it, which then needs no second kernel.
 int64_t blocks_for(int64_t T, int64_t E, bool backward) {
     int L = 1;
     while (L < 32 && L * 8 < E) L *= 2;
-    const int64_t rows = (int64_t)NW * (32 / L) * 2;
+    const int64_t turn = (int64_t)NW * (32 / L);
+    if (!backward && T <= 4 * turn) return 1;
     const int64_t most = kDesignSMs * (E > 512 ? 1 : E > 256 ? 2 : backward ? 3 : 4);
-    const int64_t b = (T + rows - 1) / rows;
+    const int64_t b = (T + 2 * turn - 1) / (2 * turn);
     return b < 1 ? 1 : b > most ? most : b;
 }
 
@@ -698,7 +773,8 @@ cudaError_t run_fwd(const FwdArgs& a, int64_t P, cudaStream_t s) {
 }
 template <typename T, int L, int R>
 cudaError_t run_bwd(const BwdArgs& a, int64_t P, cudaStream_t s) {
-    return launch(router_bwd_kernel<T, L, R>, dim3((unsigned)P), dim3(NT), bwd_smem<L, R>(), s,
+    return launch(a.renorm ? router_bwd_kernel<T, L, R, true> : router_bwd_kernel<T, L, R, false>,
+                  dim3((unsigned)P), dim3(NT), bwd_smem<L, R>(), s,
                   true, a);
 }
 
@@ -728,12 +804,12 @@ cudaError_t launch_router_fwd(const void* logits, int64_t ld, const unsigned cha
     float* part_p = (float*)workspace;
     int* part_c = (int*)(part_p + P * E);
     if (P > 0) {
-        const FwdArgs a{logits, mask, gates, ids, part_p, part_c, ld, T, (int)E, (int)k, renorm,
-                        vectors(logits, ld, (int)E, elt_bytes(dtype), T)};
+        const FwdArgs a{logits, mask, gates, ids, part_p, part_c, counts, loss, ld, (int)T, (int)E,
+                        (int)k, renorm, vectors(logits, ld, (int)E, elt_bytes(dtype), T)};
         const cudaError_t e = dtype == 0   ? ROUTER_BY_E(run_fwd, float)
                               : dtype == 1 ? ROUTER_BY_E(run_fwd, __half)
                                            : ROUTER_BY_E(run_fwd, __nv_bfloat16);
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || P == 1) return e;
     }
     const unsigned cs = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;
     return launch_cluster(router_reduce_kernel, 1, cs, dim3(RT), 0, s, (const float*)part_p,
@@ -747,7 +823,7 @@ cudaError_t launch_router_bwd(const void* logits, int64_t ld, const int* ids, co
     if (T == 0) return cudaSuccess;
     const int64_t P = blocks_for(T, E, true);
     const int es = elt_bytes(dtype);
-    const BwdArgs a{logits, ids, counts, dgates, dloss, dlogits, ld, ldd, T, (int)E, (int)k, renorm,
+    const BwdArgs a{logits, ids, counts, dgates, dloss, dlogits, ld, ldd, (int)T, (int)E, (int)k, renorm,
                     vectors(logits, ld, (int)E, es, T) && vectors(dlogits, ldd, (int)E, es, T)};
     return dtype == 0   ? ROUTER_BY_E(run_bwd, float)
            : dtype == 1 ? ROUTER_BY_E(run_bwd, __half)

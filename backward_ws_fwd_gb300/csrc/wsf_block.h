@@ -28,7 +28,7 @@ cudaError_t launch_rotary(const RotaryHeads& q, const RotaryHeads& k, const void
                           int dtype, cudaStream_t s);
 
 // Top-k router.  router_tiles: rows P of the forward's partial sums
-// (workspace: P·E floats, then P·E ints).
+// (workspace, for P > 1: P·E floats, then P·E ints).
 constexpr int64_t kRouterMaxE = 1024, kRouterMaxK = 32;
 int64_t router_tiles(int64_t T, int64_t E);
 cudaError_t launch_router_fwd(const void* logits, int64_t ld, const unsigned char* mask, int64_t k,

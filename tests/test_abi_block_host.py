@@ -83,7 +83,7 @@ def test_rotary_packed_views(wsf):
 
 def router_fwd(wsf, **over):
     a = dict(l=F, ld=64, mask=None, k=8, renorm=0, gates=2 * F, ids=3 * F, counts=4 * F,
-             loss=5 * F, ws=6 * F, wb=1 << 30, T=100, E=64, dt=wsf.BF16)
+             loss=5 * F, ws=6 * F, wb=1 << 30, T=1000, E=64, dt=wsf.BF16)
     a.update(over)
     return wsf.lib.router_fwd(_p(a["l"]), a["ld"], _p(a["mask"]), a["k"], a["renorm"], _p(a["gates"]),
                               _p(a["ids"]), _p(a["counts"]), _p(a["loss"]), _p(a["ws"]), a["wb"],
@@ -103,7 +103,7 @@ def test_router_fwd_rejects(wsf):
     for o in (dict(l=F + 1), dict(gates=2 * F + 2), dict(ids=3 * F + 1), dict(counts=4 * F + 2),
               dict(loss=5 * F + 1), dict(ws=6 * F + 2)):
         assert r(**o) == wsf.ERR_MISALIGNED, o
-    need = wsf.router_fwd_workspace_bytes(100, 64)
+    need = wsf.router_fwd_workspace_bytes(1000, 64)
     assert need > 0
     assert r(wb=need - 1) == wsf.ERR_WORKSPACE and r(ws=None) == wsf.ERR_WORKSPACE
     for o in (dict(gates=F), dict(ids=F + 4), dict(counts=3 * F), dict(loss=2 * F), dict(ws=3 * F),
@@ -198,7 +198,7 @@ def test_groupnorm_bwd_rejects(wsf):
 
 
 def test_workspace_queries(wsf):
-    assert wsf.router_fwd_workspace_bytes(0, 64) == 0
+    assert wsf.router_fwd_workspace_bytes(0, 64) == wsf.router_fwd_workspace_bytes(16, 64) == 0
     assert wsf.router_fwd_workspace_bytes(-1, 64) == wsf.SIZE_MAX
     assert wsf.router_fwd_workspace_bytes(5, 2000) == wsf.SIZE_MAX
     # bounded whatever the rows: 608 blocks of partial sums and counts
