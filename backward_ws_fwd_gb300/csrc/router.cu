@@ -359,25 +359,26 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
 #pragma unroll
             for (int q = 1; q < 8; q++) run[(r * 9 + q) * 32] = s[q];
         }
-        P* at[R];  // the heads' places
+        int at[R];  // the heads' places
 #pragma unroll
-        for (int r = 0; r < R; r++) at[r] = run + r * 9 * 32;
-        float m = 0.f;
+        for (int r = 0; r < R; r++) at[r] = r * 9 * 32;
+        P top = head[0];
         for (int j = 0; j < k; j++) {
             P b = head[0];
 #pragma unroll
             for (int r = 1; r < R; r++)
                 if (head[r].above(b)) b = head[r];
             b = b.template best<L>();
-            if (j == 0) m = key_value<T>(b.key);
+            if (j == 0) top = b;
             if (sub == 0) mine[j] = b;
 #pragma unroll
             for (int r = 0; r < R; r++) {
                 const bool won = head[r].same(b);
                 at[r] += won ? 32 : 0;
-                if (won) head[r] = *at[r];
+                if (won) head[r] = run[at[r]];
             }
         }
+        float m = key_value<T>(top.key);
         valid = valid && m != ninf();  // no logit above −inf: the row does not count
 
         // softmax, shifted by the largest
