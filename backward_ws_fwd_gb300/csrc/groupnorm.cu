@@ -28,7 +28,9 @@ namespace wsf {
 namespace {
 
 constexpr int NT = 256;
-constexpr int kFwdStages = 8, kBwdStages = 6;  // of Walk
+constexpr int kFwdStages = 8, kBwdStages = 6, kRowStages = 6;  // of Walk
+// blocks that an SM holds at once, by kernel
+constexpr int kStatsCtas = 2, kApplyCtas = 3, kBwdCtas = 2, kRowsFwdCtas = 4, kRowsBwdCtas = 3;
 
 // V consecutive values as binary32, arithmetic two lanes an instruction
 // (packed f32x2) where V > 1.
@@ -126,18 +128,31 @@ __device__ __forceinline__ void store_v(T* p, const Vals<V>& v) {
         st_stream(p, Elt<T>::narrow(f));
 }
 
+// cp.async of 16 bytes under an L2 policy.
+__device__ __forceinline__ void cp_async16_hint(void* smem, const void* gmem, uint64_t policy) {
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2;" ::"r"(s),
+                 "l"(gmem), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t l2_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // The K tensors' 16-byte vectors that one thread walks, staged S - 1 steps
 // ahead in shared memory with cp.async: a thread copies and reads only its own
 // slots, so no thread waits for another and the loads in flight do not take
-// registers.  The walk is unrolled S times (GN_WALK), which makes every slot's
-// address a constant offset.  For V == 1 (unaligned) plain loads.
+// registers.  each() unrolls the walk S times, which makes every slot's address
+// a constant offset.  For V == 1 (unaligned) plain loads.
 template <typename T, int V, int K, int S>
 struct Walk {
-    static constexpr int stages = S;
     static constexpr size_t bytes = V == 1 ? 0 : (size_t)S * K * NT * 16;
     const T* p[K];
     int64_t step[K];
     bool use[K];  // a tensor that is not used reads as zeros
+    uint64_t policy;  // of L2
     int left;     // steps not yet asked for
     Raw16* ring;
 
@@ -145,7 +160,7 @@ struct Walk {
         if (left > 0) {
 #pragma unroll
             for (int k = 0; k < K; k++) {
-                if (use[k]) cp_async16(ring + (slot * K + k) * NT, p[k], 16);
+                if (use[k]) cp_async16_hint(ring + (slot * K + k) * NT, p[k], policy);
                 p[k] += step[k];
             }
         }
@@ -181,10 +196,33 @@ struct Walk {
         }
     }
 };
-#define GN_WALK(walk, i, count)                                \
-    for (int gn_j = 0; gn_j < (count); gn_j += walk.stages)    \
-        _Pragma("unroll") for (int i = 0; i < walk.stages; i++) \
-            if (gn_j + i < (count))
+// body(vectors, step) for every step of a walk.  Whole: full turns of the ring
+// run without a condition between the steps, so that one step's arithmetic
+// fills another's latencies, where the registers for it are there.
+template <bool Whole, typename T, int V, int K, int S, typename F>
+__device__ __forceinline__ void each(Walk<T, V, K, S>& in, int count, F body) {
+    int j = 0;
+    if constexpr (Whole) {
+        for (; j + S <= count; j += S) {
+#pragma unroll
+            for (int i = 0; i < S; i++) {
+                Held<T, V> h[K];
+                in.next(i, h);
+                body(h, j + i);
+            }
+        }
+    }
+    for (; j < count; j += S) {
+#pragma unroll
+        for (int i = 0; i < S; i++) {
+            if (j + i < count) {
+                Held<T, V> h[K];
+                in.next(i, h);
+                body(h, j + i);
+            }
+        }
+    }
+}
 
 // sigmoid(z): for binary32 storage by expf and a true division, for 16-bit
 // storage by the hardware's exponential and reciprocal (together a few 2⁻²²,
@@ -231,6 +269,7 @@ struct Shape {
     int joins;     // partial statistics of a sample that the second pass joins,
     int64_t jrows; // each of jrows rows (the last: what is left)
     int lg;        // lanes that join a group's sums (a power of two)
+    int keep;      // first tile that the first pass leaves in L2 for the second
     int64_t rows;  // rows of a tile
     int64_t xstep, ystep, gstep;  // strides of the rows that a thread walks
 };
@@ -326,7 +365,7 @@ __device__ __forceinline__ Vals<V> params(const float* p, int ch) {
 // about their common mean, first the row lanes of a channel (Q threads a
 // channel where there are few), then a group's channels by lg lanes.
 template <typename T, int V>
-__global__ void __launch_bounds__(NT, 4) gn_stats_kernel(const T* x, const Shape d, float2* part) {
+__global__ void __launch_bounds__(NT, kStatsCtas) gn_stats_kernel(const T* x, const Shape d, float2* part) {
     constexpr int S = kFwdStages;
     extern __shared__ float4 smem[];
     __shared__ float part_rows[NT];              // rows of a part
@@ -353,19 +392,18 @@ __global__ void __launch_bounds__(NT, 4) gn_stats_kernel(const T* x, const Shape
             in.p[0] = base + (int64_t)t.r * d.xs + c * V;
             in.step[0] = d.xstep;
             in.use[0] = true;
+            in.policy = un.tile < d.keep ? l2_evict_first() : l2_evict_normal();
             Held<T, V> first;
             if (cnt) {
                 first.load(in.p[0]);
                 k = first.widen();
             }
             in.start(smem, cnt);
-            GN_WALK(in, i, cnt) {
-                Held<T, V> h[1];
-                in.next(i, h);
+            each<true>(in, cnt, [&](const Held<T, V>(&h)[1], int) {
                 const Vals<V> q = sub(h[0].widen(), k);
                 a = add(a, q);
                 b = fma(q, q, b);
-            }
+            });
             float m[V], e[V];
             const Vals<V> mean = mul(a, Vals<V>::splat(inv));
             add(k, mean).to(m);
@@ -377,6 +415,7 @@ __global__ void __launch_bounds__(NT, 4) gn_stats_kernel(const T* x, const Shape
             }
         }
     }
+    pdl_trigger();
     __syncthreads();
     if (t.RL > 1 && pt.q < pt.Q) {  // into row lane q
         const float n = part_rows[pt.q], inv = n > 0.f ? 1.0f / n : 0.f;
@@ -415,7 +454,6 @@ __global__ void __launch_bounds__(NT, 4) gn_stats_kernel(const T* x, const Shape
         s = lanes_sum(s, d.lg);
         if (on && j0 == 0) part[(int64_t)blockIdx.x * d.G + g] = make_float2(m, s);
     }
-    pdl_trigger();
 }
 
 // Where a sample has many tiles, their statistics (or the backward's sums) are
@@ -457,7 +495,7 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(const float2* part, float2*
 // Second pass.  The block first joins its sample's partial statistics, lg
 // lanes a group; the first tile's block writes the statistics out.
 template <typename T, int V, bool Silu>
-__global__ void __launch_bounds__(NT, 3) gn_apply_kernel(const T* x, T* y, const float* w,
+__global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T* y, const float* w,
                                                       const float* b, float eps, float* mean,
                                                       float* rstd, const float2* part,
                                                       const Shape d) {
@@ -471,6 +509,7 @@ __global__ void __launch_bounds__(NT, 3) gn_apply_kernel(const T* x, T* y, const
         in.p[0] = x + un.n * d.xn + (un.s0 + t.r) * d.xs + c * V;
         in.step[0] = d.xstep;
         in.use[0] = true;
+        in.policy = l2_evict_first();  // the last use
         in.start(smem, cnt);
     };
     pdl_wait();
@@ -513,12 +552,10 @@ __global__ void __launch_bounds__(NT, 3) gn_apply_kernel(const T* x, T* y, const
                                    params<V>(w, c * V));
             const Vals<V> sh = params<V>(b, c * V);
             T* o = y + un.n * d.yn + (un.s0 + t.r) * d.ys + c * V;
-            GN_WALK(in, i, cnt) {
-                Held<T, V> h[1];
-                in.next(i, h);
+            each<true>(in, cnt, [&](const Held<T, V>(&h)[1], int) {
                 store_v<T, V>(o, activate<T, Silu, V>(fma(sub(h[0].widen(), mu), rw, sh)));
                 o += d.ystep;
-            }
+            });
         }
     }
     pdl_trigger();
@@ -528,7 +565,7 @@ __global__ void __launch_bounds__(NT, 3) gn_apply_kernel(const T* x, T* y, const
 // Backward, first pass: a block walks units u0 .. u1 and writes each unit's
 // groups' sums (shares of M·m₂ and M·m₁) and, over all of them, the channels'.
 template <typename T, int V, bool Silu>
-__global__ void __launch_bounds__(NT, 3) gn_bwd_sums_kernel(const T* x, const T* dy, const float* w,
+__global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, const T* dy, const float* w,
                                                          const float* b, const float* mean,
                                                          const float* rstd, const Shape d,
                                                          float2* part_g, float* part_a,
@@ -558,20 +595,19 @@ __global__ void __launch_bounds__(NT, 3) gn_bwd_sums_kernel(const T* x, const T*
                 in.step[0] = d.xstep;
                 in.step[1] = d.gstep;
                 in.use[0] = in.use[1] = true;
+                in.policy = un.tile < d.keep ? l2_evict_first() : l2_evict_normal();
                 in.start(smem, cnt);
                 const Vals<V> mu = by_group<V>(c * V, d.Cg, [&](int g) { return __ldg(mn + g); });
                 const Vals<V> rw = mul(by_group<V>(c * V, d.Cg, [&](int g) { return __ldg(rn + g); }),
                                        params<V>(w, c * V));
                 const Vals<V> bc = params<V>(b, c * V);
                 Vals<V> A = Vals<V>::splat(0.f), B = A;
-                GN_WALK(in, i, cnt) {
-                    Held<T, V> h[2];
-                    in.next(i, h);
+                each<true>(in, cnt, [&](const Held<T, V>(&h)[2], int) {
                     const Vals<V> f = sub(h[0].widen(), mu);
                     const Vals<V> dz = through<T, Silu, V>(h[1].widen(), fma(f, rw, bc));
                     A = fma(dz, f, A);  // times r below
                     B = add(B, dz);
-                }
+                });
                 float fa[V], fb[V];
                 mul(A, by_group<V>(c * V, d.Cg, [&](int g) { return __ldg(rn + g); })).to(fa);
                 B.to(fb);
@@ -582,6 +618,7 @@ __global__ void __launch_bounds__(NT, 3) gn_bwd_sums_kernel(const T* x, const T*
                 }
             }
         }
+        if (u + 1 == u1) pdl_trigger();
         __syncthreads();
         if (pt.Q > 1 && pt.q < pt.Q) {  // into row lane q
             const int c = (int)threadIdx.x - pt.q * d.C;
@@ -613,12 +650,11 @@ __global__ void __launch_bounds__(NT, 3) gn_bwd_sums_kernel(const T* x, const T*
         }
         __syncthreads();
     }
-    pdl_trigger();
 }
 
 // dx = dz·(w·r) − (x − μ)·(r²·m₂) − r·m₁
 template <typename T, int V, bool Silu>
-__global__ void __launch_bounds__(NT, 3) gn_bwd_apply_kernel(const T* x, const T* dy, T* dx,
+__global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_apply_kernel(const T* x, const T* dy, T* dx,
                                                           const float* w, const float* b,
                                                           const float* mean, const float* rstd,
                                                           const float2* part, const Shape d) {
@@ -635,6 +671,7 @@ __global__ void __launch_bounds__(NT, 3) gn_bwd_apply_kernel(const T* x, const T
         in.step[0] = d.xstep;
         in.step[1] = d.gstep;
         in.use[0] = in.use[1] = true;
+        in.policy = l2_evict_first();  // the last use
         in.start(smem, cnt);
     };
     pdl_wait();
@@ -672,14 +709,12 @@ __global__ void __launch_bounds__(NT, 3) gn_bwd_apply_kernel(const T* x, const T
             const Vals<V> e2 = by_group<V>(c * V, d.Cg, [&](int g) { return st[g].w; });
             const Vals<V> bc = params<V>(b, c * V);
             T* o = dx + un.n * d.yn + (un.s0 + t.r) * d.ys + c * V;
-            GN_WALK(in, i, cnt) {
-                Held<T, V> h[2];
-                in.next(i, h);
+            each<true>(in, cnt, [&](const Held<T, V>(&h)[2], int) {
                 const Vals<V> f = sub(h[0].widen(), mu);
                 const Vals<V> dz = through<T, Silu, V>(h[1].widen(), fma(f, rw, bc));
                 store_v<T, V>(o, fma(dz, rw, fma(f, e2, e1)));
                 o += d.ystep;
-            }
+            });
         }
     }
     pdl_trigger();
@@ -757,7 +792,7 @@ struct Place {
 };
 
 template <typename T, int CPL, bool Silu>
-__global__ void __launch_bounds__(RT, CPL == 1 ? 4 : 2)
+__global__ void __launch_bounds__(RT, CPL == 1 ? kRowsFwdCtas : 2)
     gn_rows_fwd_kernel(const T* x, T* y, const float* w, const float* b, float eps, float* mean,
                        float* rstd, const RowShape d) {
     constexpr int V = Elt<T>::V;
@@ -787,12 +822,10 @@ __global__ void __launch_bounds__(RT, CPL == 1 ? 4 : 2)
         in.step[c] = d.xstep;
         in.use[c] = has[c];
     }
+    in.policy = l2_evict_first();
     in.start(smem, mine);
     T* o = y + n * d.yn + t.at;
-    GN_WALK(in, i, turns) {
-        const int turn = gn_j + i;
-        Held<T, V> h[CPL];
-        in.next(i, h);
+    each<true>(in, turns, [&](Held<T, V>(&h)[CPL], int turn) {
         Vals<V> f[CPL], q = Vals<V>::splat(0.f);
 #pragma unroll
         for (int c = 0; c < CPL; c++) {
@@ -821,33 +854,56 @@ __global__ void __launch_bounds__(RT, CPL == 1 ? 4 : 2)
         }
         n += d.step;
         o += d.ystep;
-    }
+    });
     pdl_trigger();
 }
 
 template <typename T, int CPL, bool Silu>
-__global__ void __launch_bounds__(RT, CPL == 1 ? 3 : 2)
+__global__ void __launch_bounds__(RT, CPL == 1 ? kRowsBwdCtas : 2)
     gn_rows_bwd_kernel(const T* x, const T* dy, T* dx, const float* w, const float* b,
                        const float* mean, const float* rstd, float* part_a, float* part_b,
                        const RowShape d) {
-    constexpr int V = Elt<T>::V, S = CPL == 1 ? kBwdStages : kBwdStages / 2;
+    constexpr int V = Elt<T>::V, S = CPL == 1 ? kRowStages : kRowStages / 2;
     extern __shared__ float4 smem[];
     float* sum = reinterpret_cast<float*>(smem);  // [2][RW][CPL][V][32], in place of the staging
     const Place t(d, V);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const float inv = 1.0f / (float)d.Cg;
     bool has[CPL];
-    Vals<V> wc[CPL], bc[CPL], A[CPL], B[CPL];
+    Vals<V> A[CPL], B[CPL];
+    // w and b of the block's places, in shared memory: in registers they would
+    // leave room for three blocks an SM in place of four
+    float4* wb = smem + Walk<T, V, 2 * CPL, S>::bytes / 16 + lane;  // [w, b][CPL][V / 4][32]
     pdl_wait();
 #pragma unroll
     for (int c = 0; c < CPL; c++) {
         has[c] = t.on && t.j + c * d.lpg < d.cpg;
-        wc[c] = bc[c] = A[c] = B[c] = Vals<V>::splat(0.f);
-        if (has[c]) {
-            wc[c] = params<V>(w, t.at + c * d.lpg * V);
-            bc[c] = params<V>(b, t.at + c * d.lpg * V);
-        }
+        A[c] = B[c] = Vals<V>::splat(0.f);
     }
+    if (wid < 2) {
+        const float* p = (wid ? b : w) + t.at;
+#pragma unroll
+        for (int c = 0; c < CPL; c++)
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (has[c]) {
+                    const float* r = p + c * d.lpg * V + i;
+                    q = make_float4(__ldg(r), __ldg(r + 1), __ldg(r + 2), __ldg(r + 3));
+                }
+                wb[((wid * CPL + c) * (V / 4) + i / 4) * 32] = q;
+            }
+    }
+    __syncthreads();
+    auto param = [&](int which, int c) {
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 q = wb[((which * CPL + c) * (V / 4) + i / 4) * 32];
+            f[i] = q.x, f[i + 1] = q.y, f[i + 2] = q.z, f[i + 3] = q.w;
+        }
+        return Vals<V>::of(f);
+    };
     int64_t n = ((int64_t)(blockIdx.x / d.segs) * RW + wid) * d.rpw;
     const int turns = n < d.N ? (int)((d.N - 1 - n) / d.step) + 1 : 0;  // of the warp
     n += t.sub;
@@ -862,15 +918,13 @@ __global__ void __launch_bounds__(RT, CPL == 1 ? 3 : 2)
         in.step[2 * c + 1] = d.gstep;
         in.use[2 * c] = in.use[2 * c + 1] = has[c];
     }
+    in.policy = l2_evict_first();
     in.start(smem, mine);
     T* o = dx + n * d.yn + t.at;
     // the statistics, a turn ahead
     const float *mp = mean + (mine ? n : 0) * d.G + t.g, *rp = rstd + (mine ? n : 0) * d.G + t.g;
     float mu = __ldg(mp), rs = __ldg(rp);
-    GN_WALK(in, i, turns) {
-        const int turn = gn_j + i;
-        Held<T, V> h[2 * CPL];
-        in.next(i, h);
+    each<true>(in, turns, [&](Held<T, V>(&h)[2 * CPL], int turn) {
         const float m0 = mu, r0 = rs;
         if (turn + 1 < mine) {
             mp += d.step * d.G;
@@ -884,10 +938,12 @@ __global__ void __launch_bounds__(RT, CPL == 1 ? 3 : 2)
             // absent lanes: dy = 0 keeps them out of every sum
             if (d.rpw > 1 && turn >= mine) h[2 * c].raw = h[2 * c + 1].raw = raw_zero();
             xh[c] = fma(h[2 * c].widen(), Vals<V>::splat(r0), Vals<V>::splat(-m0 * r0));
-            const Vals<V> dz = through<T, Silu, V>(h[2 * c + 1].widen(), fma(xh[c], wc[c], bc[c]));
+            const Vals<V> wc = param(0, c);
+            const Vals<V> dz =
+                through<T, Silu, V>(h[2 * c + 1].widen(), fma(xh[c], wc, param(1, c)));
             A[c] = fma(dz, xh[c], A[c]);
             B[c] = add(B[c], dz);
-            g[c] = mul(dz, wc[c]);
+            g[c] = mul(dz, wc);
             s1 = add(s1, g[c]);
             s2 = fma(g[c], xh[c], s2);
         }
@@ -902,7 +958,7 @@ __global__ void __launch_bounds__(RT, CPL == 1 ? 3 : 2)
                     store_v<T, V>(o + c * d.lpg * V, fma(g[c], r, fma(xh[c], e2, e1)));
         }
         o += d.ystep;
-    }
+    });
     __syncthreads();
     // the block's sums, over its warps and a warp's rows in order
 #pragma unroll
@@ -943,11 +999,10 @@ void tile(Shape& d, int64_t chunk, int64_t blocks, int es) {
     d.tiles = (int)((d.S + rows - 1) / rows);
 }
 
-constexpr int64_t kStatsBlocks = kDesignSMs * 4, kBlocks = kDesignSMs * 3;
-
 // chunk: samples of one pair of passes, whose tensors (x, or x and dy) fit in
-// L2.  The tiles are the first pass's.
-constexpr int64_t kL2Chunk = 64 << 20;
+// L2.  The tiles are the first pass's.  Of a sample that does not fit, the
+// first pass keeps the end, which the second pass reads first.
+constexpr int64_t kL2Chunk = 96 << 20, kL2Keep = 64 << 20;
 
 Shape shape_of(int64_t N, int64_t S, int64_t C, int64_t G, int es, bool backward, int64_t& chunk) {
     Shape d{};
@@ -959,7 +1014,9 @@ Shape shape_of(int64_t N, int64_t S, int64_t C, int64_t G, int es, bool backward
     chunk = std::min(N, std::max<int64_t>(1, kL2Chunk / sample));
     chunk = (N + (N + chunk - 1) / chunk - 1) / ((N + chunk - 1) / chunk);  // even chunks
     d.N = chunk;
-    tile(d, chunk, backward ? kBlocks : kStatsBlocks, es);
+    tile(d, chunk, kDesignSMs * (backward ? kBwdCtas : kStatsCtas), es);
+    if (chunk == 1 && sample > kL2Keep)
+        d.keep = (int)(d.tiles - d.tiles * kL2Keep / sample);
     d.joins = d.tiles > kJoin ? 1 : d.tiles;
     d.jrows = d.tiles > kJoin ? S : d.rows;
     d.lg = 32;
@@ -976,7 +1033,7 @@ void steps(Shape& d, int V) {
 
 // Blocks of the backward's first pass: rows of the channels' partial sums.
 int64_t grad_rows(const Shape& d) {
-    return std::min<int64_t>(d.N * d.tiles, kBlocks);
+    return std::min<int64_t>(d.N * d.tiles, kDesignSMs * kBwdCtas);
 }
 
 int64_t pad64(int64_t n) { return (n + 63) / 64 * 64; }
@@ -1015,7 +1072,7 @@ bool row_shape(int64_t N, int64_t S, int64_t C, int64_t G, int es, bool backward
     // blocks along the samples: as many as the SMs hold at once, fewer where
     // warps would stand idle
     const int64_t per = (int64_t)RW * d.rpw, need = (N + per - 1) / per;
-    const int64_t most = kDesignSMs * (cpl == 2 ? 2 : backward ? 3 : 4) / d.segs;
+    const int64_t most = kDesignSMs * (cpl == 2 ? 2 : backward ? kRowsBwdCtas : kRowsFwdCtas) / d.segs;
     d.RB = (int)(need < most ? need : most < 1 ? 1 : most);
     d.step = (int64_t)d.RB * per;
     return true;
@@ -1036,8 +1093,9 @@ cudaError_t rows_bwd(const GroupNormBwd& a, const RowShape& d, bool silu, cudaSt
     float* pa = (float*)a.workspace;
     float* pb = pa + pad64((int64_t)d.RB * d.C);
     const auto k = silu ? gn_rows_bwd_kernel<T, CPL, true> : gn_rows_bwd_kernel<T, CPL, false>;
-    constexpr size_t stage = Walk<T, Elt<T>::V, 2 * CPL, CPL == 1 ? kBwdStages : kBwdStages / 2>::bytes;
-    constexpr size_t smem = std::max(stage, (size_t)2 * RW * CPL * Elt<T>::V * 32 * 4);
+    constexpr size_t stage = Walk<T, Elt<T>::V, 2 * CPL, CPL == 1 ? kRowStages : kRowStages / 2>::bytes;
+    constexpr size_t smem = std::max(stage, (size_t)2 * RW * CPL * Elt<T>::V * 32 * 4) +
+                            (size_t)2 * CPL * Elt<T>::V * 32 * 4;
     cudaError_t e = allow(k, smem);
     if (e == cudaSuccess)
         e = launch(k, dim3((unsigned)(d.segs * d.RB)), dim3(RT), smem, s, true, (const T*)a.x,
@@ -1063,7 +1121,7 @@ cudaError_t fwd(const GroupNormFwd& a, Shape d, int64_t chunk, bool silu, cudaSt
     if (e == cudaSuccess) e = allow(apply, smem2);
     steps(d, V);
     Shape d2 = d;
-    tile(d2, chunk, kBlocks, (int)sizeof(T));
+    tile(d2, chunk, kDesignSMs * kApplyCtas, (int)sizeof(T));
     for (int64_t n = 0; n < a.N && e == cudaSuccess; n += chunk) {
         d.N = d2.N = std::min(chunk, a.N - n);
         const T* x = (const T*)a.x + n * d.xn;
