@@ -6,7 +6,6 @@ checked here (TypeError, ValueError); the rest is checked there (WsfError).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -14,9 +13,8 @@ from . import SIZE_MAX, _check, _dtype_code, _scratch, lib
 
 _vp, _i64, _int, _sz, _f = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t,
                             ctypes.c_float)
-_st3 = _i64 * 3
-_stp = ctypes.POINTER(_i64)
-_ROTARY = [_vp, _stp, _vp, _stp, _i64, _vp, _stp, _vp, _stp, _i64, _vp, _i64, _int, _vp, _f, _int,
+_st12 = _i64 * 12
+_ROTARY = [_vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _int, _vp, _f, _int,
            _i64, _i64, _i64, _i64, _int, _vp]
 for _fn in (lib.rotary_fwd, lib.rotary_bwd):
     _fn.argtypes, _fn.restype = _ROTARY, _int
@@ -74,17 +72,20 @@ def _like(t, name, x):
         _refuse(t, name, x.dtype, x.shape, x.device)
 
 
-def _at(stream, t):
-    """Context that makes t's device current, and the raw stream to launch on."""
+def _launch(call, what, t, stream, *args):
+    """call(*args, stream) with t's device current."""
     import torch
     dev = t.get_device()
-    if dev < 0:  # host memory: the library or CUDA refuses it
-        return contextlib.nullcontext(), None
+    if dev < 0:  # host memory, which the library cannot tell from the device's
+        raise ValueError(f"{what}: the tensors are not on a GPU")
     raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    return (_HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)), raw
-
-
-_HERE = contextlib.nullcontext()
+    if torch.cuda.current_device() == dev:
+        rc = call(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            rc = call(*args, raw)
+    if rc:
+        _check(rc, what)
 
 
 def _p(t):
@@ -93,11 +94,11 @@ def _p(t):
 
 
 def _work(need, workspace, t, stream):
-    """(address, bytes) of the caller's workspace, or of a temporary one."""
-    if workspace is None and need not in (0, SIZE_MAX):
-        workspace = _scratch(need, t.device, stream)
+    """(address, bytes, tensor) of the caller's workspace, or of a temporary one."""
     if workspace is None:
-        return None, 0, None
+        if need == 0 or need == SIZE_MAX:
+            return None, 0, None
+        workspace = _scratch(need, t.device, stream)
     return _p(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -106,7 +107,7 @@ def _work(need, workspace, t, stream):
 
 def _strides3(t):
     s = t.stride()
-    return _st3(s[0], s[1], s[2]) if len(s) == 4 else _st3(0, s[0], s[1])
+    return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
 def _rotary(call, what, q, k, positions, inv_freq, scale, interleaved, q_out, k_out, stream):
@@ -118,46 +119,54 @@ def _rotary(call, what, q, k, positions, inv_freq, scale, interleaved, q_out, k_
         B, (S, H, D) = 1, shape
     else:
         raise ValueError("heads must be [B, S, H, D] or [T, H, D]")
-    dev, code = q.device, _dtype_code(q)
-    _like(q, "q", q)
+    dev, dtype, code = q.device, q.dtype, _dtype_code(q)
+    if q.stride(-1) != 1 and D > 1:
+        _refuse(q, "q", None, None, dev)
     if q_out is None:
         q_out = torch.empty_like(q)
     else:
         _like(q_out, "q_out", q)
     R = 2 * inv_freq.numel()
-    _want(inv_freq, "inv_freq", torch.float32, (R // 2,), dev)
-    Hk = 0
+    if not _fits(inv_freq, torch.float32, (R // 2,), dev):
+        _refuse(inv_freq, "inv_freq", torch.float32, (R // 2,), dev)
+    sq, so = _strides3(q), _strides3(q_out)
+    Hk, sk, sp = 0, _NONE3, _NONE3
     if k is not None:
-        Hk = k.shape[-2]
-        if k.shape[:-2] != shape[:-2] or k.shape[-1] != D:
-            raise ValueError(f"k {list(k.shape)} does not go with q {list(shape)}")
-        if k.dtype != q.dtype or k.device != dev or (k.stride(-1) != 1 and D > 1):
-            _refuse(k, "k", q.dtype, None, dev)
+        ks = k.shape
+        if len(ks) != len(shape) or ks[0] != shape[0] or ks[-1] != D or ks[:-2] != shape[:-2]:
+            raise ValueError(f"k {list(ks)} does not go with q {list(shape)}")
+        if k.dtype != dtype or k.device != dev or (k.stride(-1) != 1 and D > 1):
+            _refuse(k, "k", dtype, None, dev)
         if k_out is None:
             k_out = torch.empty_like(k)
         else:
             _like(k_out, "k_out", k)
+        Hk, sk, sp = ks[-2], _strides3(k), _strides3(k_out)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    pb = 8 if positions.dtype == torch.int64 else 4
     ps = positions.shape
     ldp = 0
     if len(ps) == 2 and ps[0] == B and ps[1] == S and len(shape) == 4:
         ldp = positions.stride(0) if B > 1 else 0
     elif ps != (S,) and not (len(shape) == 4 and ps == (1, S)):
         raise ValueError(f"positions {list(ps)} do not go with q {list(shape)}")
-    if pb == 4 and positions.dtype != torch.int32:
+    if positions.dtype == torch.int64:
+        pb = 8
+    elif positions.dtype == torch.int32:
+        pb = 4
+    else:
         raise TypeError(f"positions must be int32 or int64, not {positions.dtype}")
     if positions.device != dev or (S > 1 and positions.stride(-1) != 1):
         _refuse(positions, "positions", None, None, dev)
-    on, raw = _at(stream, q)
-    with on:
-        rc = call(_p(q), _strides3(q), _p(q_out), _strides3(q_out), H, _p(k),
-                  _strides3(k) if Hk else None, _p(k_out), _strides3(k_out) if Hk else None, Hk,
-                  _p(positions), ldp, pb, _p(inv_freq), scale, 1 if interleaved else 0, B, S, D,
-                  R, code, raw)
-    _check(rc, what)
+    strides = _st12(*sq, *so, *sk, *sp)  # read before the call returns
+    at = ctypes.addressof(strides)
+    _launch(call, what, q, stream, _p(q), at, _p(q_out), at + 24, H, _p(k), at + 48, _p(k_out),
+            at + 72, Hk, _p(positions), ldp, pb, _p(inv_freq), scale, 1 if interleaved else 0, B,
+            S, D, R, code)
     return q_out, k_out
+
+
+_NONE3 = (0, 0, 0)
 
 
 def rotary_fwd(q, k, positions, inv_freq, scale=1.0, interleaved=False, q_out=None, k_out=None,
@@ -256,12 +265,10 @@ def router_fwd(logits, k, mask=None, renormalize=False, gates=None, ids=None, co
         loss = torch.empty((), dtype=torch.float32, device=dev)
     else:
         _want(loss, "loss", torch.float32, (), dev)
-    on, raw = _at(stream, logits)
-    with on:
-        ws, wbytes, keep = _work(lib.router_fwd_workspace_bytes(T, E), workspace, logits, stream)
-        rc = lib.router_fwd(_p(logits), logits.stride(0), _p(mask), k, 1 if renormalize else 0,
-                            _p(gates), _p(ids), _p(counts), _p(loss), ws, wbytes, T, E, code, raw)
-    _check(rc, "router_fwd")
+    ws, wbytes, keep = _work(lib.router_fwd_workspace_bytes(T, E), workspace, logits, stream)
+    _launch(lib.router_fwd, "router_fwd", logits, stream, _p(logits), logits.stride(0), _p(mask),
+            k, 1 if renormalize else 0, _p(gates), _p(ids), _p(counts), _p(loss), ws, wbytes, T, E,
+            code)
     return gates, ids, counts, loss
 
 
@@ -284,12 +291,9 @@ def router_bwd(logits, ids, counts, dgates, dloss, renormalize=False, dlogits=No
         dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
     else:
         _like(dlogits, "dlogits", logits)
-    on, raw = _at(stream, logits)
-    with on:
-        rc = lib.router_bwd(_p(logits), logits.stride(0), _p(ids), _p(counts), k,
-                            1 if renormalize else 0, _p(dgates), _p(dloss), _p(dlogits),
-                            dlogits.stride(0), T, E, code, raw)
-    _check(rc, "router_bwd")
+    _launch(lib.router_bwd, "router_bwd", logits, stream, _p(logits), logits.stride(0), _p(ids),
+            _p(counts), k, 1 if renormalize else 0, _p(dgates), _p(dloss), _p(dlogits),
+            dlogits.stride(0), T, E, code)
     return dlogits
 
 
@@ -351,14 +355,11 @@ def groupnorm_fwd(x, w, b, groups, eps=1e-5, act=None, y=None, mean=None, rstd=N
         rstd = torch.empty((N, groups), dtype=torch.float32, device=dev)
     else:
         _want(rstd, "rstd", torch.float32, (N, groups), dev)
-    on, raw = _at(stream, x)
-    with on:
-        ws, wbytes, keep = _work(lib.groupnorm_fwd_workspace_bytes(N, S, C, groups, code),
-                                 workspace, x, stream)
-        rc = lib.groupnorm_fwd(_p(x), *_ns_strides(x), _p(w), _p(b), eps, act, _p(y),
-                               *_ns_strides(y), _p(mean), _p(rstd), ws, wbytes, N, S, C, groups,
-                               code, raw)
-    _check(rc, "groupnorm_fwd")
+    ws, wbytes, keep = _work(lib.groupnorm_fwd_workspace_bytes(N, S, C, groups, code), workspace, x,
+                             stream)
+    _launch(lib.groupnorm_fwd, "groupnorm_fwd", x, stream, _p(x), *_ns_strides(x), _p(w), _p(b),
+            eps, act, _p(y), *_ns_strides(y), _p(mean), _p(rstd), ws, wbytes, N, S, C, groups,
+            code)
     return y, mean, rstd
 
 
@@ -387,13 +388,9 @@ def groupnorm_bwd(x, w, b, mean, rstd, dy, groups, act=None, dx=None, grad_w=Non
         grad_b = torch.empty(C, dtype=torch.float32, device=dev)
     else:
         _want(grad_b, "grad_b", torch.float32, (C,), dev)
-    on, raw = _at(stream, x)
-    with on:
-        ws, wbytes, keep = _work(lib.groupnorm_bwd_workspace_bytes(N, S, C, groups, code),
-                                 workspace, x, stream)
-        rc = lib.groupnorm_bwd(_p(x), *_ns_strides(x), _p(w), _p(b), _p(mean), _p(rstd), _p(dy),
-                               *_ns_strides(dy), act, _p(dx), *_ns_strides(dx), _p(grad_w),
-                               _p(grad_b), 1 if accumulate else 0, ws, wbytes, N, S, C, groups,
-                               code, raw)
-    _check(rc, "groupnorm_bwd")
+    ws, wbytes, keep = _work(lib.groupnorm_bwd_workspace_bytes(N, S, C, groups, code), workspace, x,
+                             stream)
+    _launch(lib.groupnorm_bwd, "groupnorm_bwd", x, stream, _p(x), *_ns_strides(x), _p(w), _p(b),
+            _p(mean), _p(rstd), _p(dy), *_ns_strides(dy), act, _p(dx), *_ns_strides(dx),
+            _p(grad_w), _p(grad_b), 1 if accumulate else 0, ws, wbytes, N, S, C, groups, code)
     return dx, grad_w, grad_b

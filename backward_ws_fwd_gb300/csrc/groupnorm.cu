@@ -365,7 +365,8 @@ __device__ __forceinline__ Vals<V> params(const float* p, int ch) {
 // about their common mean, first the row lanes of a channel (Q threads a
 // channel where there are few), then a group's channels by lg lanes.
 template <typename T, int V>
-__global__ void __launch_bounds__(NT, kStatsCtas) gn_stats_kernel(const T* x, const Shape d, float2* part) {
+__global__ void __launch_bounds__(NT, kStatsCtas) gn_stats_kernel(const T* x, const Shape d, float* part_m,
+                                                               float* part_q) {
     constexpr int S = kFwdStages;
     extern __shared__ float4 smem[];
     __shared__ float part_rows[NT];              // rows of a part
@@ -452,7 +453,10 @@ __global__ void __launch_bounds__(NT, kStatsCtas) gn_stats_kernel(const T* x, co
                     s += fmaf(part_rows[q] * e, e, sq[q * d.C + g * d.Cg + c]);
                 }
         s = lanes_sum(s, d.lg);
-        if (on && j0 == 0) part[(int64_t)blockIdx.x * d.G + g] = make_float2(m, s);
+        if (on && j0 == 0) {
+            part_m[(int64_t)blockIdx.x * d.G + g] = m;
+            part_q[(int64_t)blockIdx.x * d.G + g] = s;
+        }
     }
 }
 
@@ -461,44 +465,45 @@ __global__ void __launch_bounds__(NT, kStatsCtas) gn_stats_kernel(const T* x, co
 constexpr int kJoin = 48;  // partials that the second pass joins itself
 
 template <bool Sums>
-__global__ void __launch_bounds__(NT) gn_join_kernel(const float2* part, float2* out,
-                                                     const Shape d) {
+__global__ void __launch_bounds__(NT) gn_join_kernel(const float* pm, const float* pq, float* om,
+                                                     float* oq, const Shape d) {
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int64_t u = (int64_t)blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
     if (u < d.N * d.G) {
-        const float2* p = part + u / d.G * d.tiles * d.G + u % d.G;
+        pm += u / d.G * d.tiles * d.G + u % d.G;
+        pq += u / d.G * d.tiles * d.G + u % d.G;
         const float whole = (float)d.rows, last = (float)(d.S - (d.tiles - 1) * d.rows);
         float s = 0.f, q = 0.f;
 #pragma unroll 8
         for (int i = lane; i < d.tiles; i += 32) {
-            const float2 v = p[(int64_t)i * d.G];
-            s = fmaf(Sums ? 1.f : i + 1 < d.tiles ? whole : last, v.x, s);
-            if (Sums) q += v.y;
+            s = fmaf(Sums ? 1.f : i + 1 < d.tiles ? whole : last, pm[(int64_t)i * d.G], s);
+            if (Sums) q += pq[(int64_t)i * d.G];
         }
         s = group_sum<32>(s);
         if (!Sums) {
             s /= (float)d.S;
 #pragma unroll 8
             for (int i = lane; i < d.tiles; i += 32) {
-                const float2 v = p[(int64_t)i * d.G];
-                const float e = v.x - s;
-                q += fmaf((i + 1 < d.tiles ? whole : last) * d.Cg * e, e, v.y);
+                const float e = pm[(int64_t)i * d.G] - s;
+                q += fmaf((i + 1 < d.tiles ? whole : last) * d.Cg * e, e, pq[(int64_t)i * d.G]);
             }
         }
         q = group_sum<32>(q);
-        if (lane == 0) out[u] = make_float2(s, q);
+        if (lane == 0) om[u] = s, oq[u] = q;
     }
     pdl_trigger();
 }
 
 // Second pass.  The block first joins its sample's partial statistics, lg
-// lanes a group; the first tile's block writes the statistics out.
+// lanes a group; the first tile's block writes the statistics out.  (Samples of
+// one tile keep their partial statistics where the results go: the one block
+// that reads them replaces them.)
 template <typename T, int V, bool Silu>
 __global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T* y, const float* w,
                                                       const float* b, float eps, float* mean,
-                                                      float* rstd, const float2* part,
-                                                      const Shape d) {
+                                                      float* rstd, const float* part_m,
+                                                      const float* part_q, const Shape d) {
     extern __shared__ float4 smem[];
     Walk<T, V, 1, kFwdStages> in;
     float2* st = reinterpret_cast<float2*>(smem) + in.bytes / 8;  // [G] μ, r
@@ -518,22 +523,22 @@ __global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T*
     for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
         const int g = g0 + threadIdx.x / d.lg;
         const bool on = g < d.G;
-        const float2* p = part + (int64_t)un.n * d.joins * d.G + g;
+        const float* pm = part_m + (int64_t)un.n * d.joins * d.G + g;
+        const float* pq = part_q + (int64_t)un.n * d.joins * d.G + g;
         const float whole = (float)d.jrows, last = (float)(d.S - (d.joins - 1) * d.jrows);
         float s = 0.f;
         if (on) {
 #pragma unroll 4
             for (int i = j0; i < d.joins; i += d.lg)
-                s = fmaf(i + 1 < d.joins ? whole : last, p[(int64_t)i * d.G].x, s);
+                s = fmaf(i + 1 < d.joins ? whole : last, pm[(int64_t)i * d.G], s);
         }
         const float m = lanes_sum(s, d.lg) / (float)d.S;
         s = 0.f;
         if (on) {
 #pragma unroll 4
             for (int i = j0; i < d.joins; i += d.lg) {
-                const float2 q = p[(int64_t)i * d.G];
-                const float e = q.x - m;
-                s += fmaf((i + 1 < d.joins ? whole : last) * d.Cg * e, e, q.y);
+                const float e = pm[(int64_t)i * d.G] - m;
+                s += fmaf((i + 1 < d.joins ? whole : last) * d.Cg * e, e, pq[(int64_t)i * d.G]);
             }
         }
         s = lanes_sum(s, d.lg);
@@ -568,7 +573,7 @@ template <typename T, int V, bool Silu>
 __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, const T* dy, const float* w,
                                                          const float* b, const float* mean,
                                                          const float* rstd, const Shape d,
-                                                         float2* part_g, float* part_a,
+                                                         float* part_1, float* part_2, float* part_a,
                                                          float* part_b) {
     extern __shared__ float4 smem[];
     const Lanes t(d.C, V);
@@ -646,7 +651,10 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, c
                 for (int c = j0; c < d.Cg; c += d.lg) A += sa[g * d.Cg + c], B += sb[g * d.Cg + c];
             A = lanes_sum(A, d.lg);
             B = lanes_sum(B, d.lg);
-            if (g < d.G && j0 == 0) part_g[(int64_t)u * d.G + g] = make_float2(A, B);
+            if (g < d.G && j0 == 0) {
+                part_1[(int64_t)u * d.G + g] = B;
+                part_2[(int64_t)u * d.G + g] = A;
+            }
         }
         __syncthreads();
     }
@@ -657,7 +665,8 @@ template <typename T, int V, bool Silu>
 __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_apply_kernel(const T* x, const T* dy, T* dx,
                                                           const float* w, const float* b,
                                                           const float* mean, const float* rstd,
-                                                          const float2* part, const Shape d) {
+                                                          const float* part_1, const float* part_2,
+                                                          const Shape d) {
     extern __shared__ float4 smem[];
     Walk<T, V, 2, kBwdStages> in;
     float4* st = smem + in.bytes / 16;  // [G] μ, r, −r·m₁, −r²·m₂
@@ -681,14 +690,14 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_apply_kernel(const T* x, 
     for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
         const int g = g0 + threadIdx.x / d.lg;
         const bool on = g < d.G;
-        const float2* p = part + (int64_t)un.n * d.joins * d.G + g;
+        const float* p1 = part_1 + (int64_t)un.n * d.joins * d.G + g;
+        const float* p2 = part_2 + (int64_t)un.n * d.joins * d.G + g;
         float A = 0.f, B = 0.f;
         if (on) {
 #pragma unroll 4
             for (int i = j0; i < d.joins; i += d.lg) {
-                const float2 q = p[(int64_t)i * d.G];
-                A += q.x;
-                B += q.y;
+                A += p2[(int64_t)i * d.G];
+                B += p1[(int64_t)i * d.G];
             }
         }
         A = lanes_sum(A, d.lg);
@@ -1108,12 +1117,13 @@ cudaError_t rows_bwd(const GroupNormBwd& a, const RowShape& d, bool silu, cudaSt
 
 dim3 join_grid(const Shape& d) { return dim3((unsigned)((d.N * d.G + NT / 32 - 1) / (NT / 32))); }
 
-// Partial statistics of a chunk's tiles, and of its samples.
-int64_t part_floats(const Shape& d, int64_t chunk) { return pad64(2 * chunk * (d.tiles + 1) * d.G); }
+// One plane of the partial statistics of a chunk's tiles, and of its samples.
+int64_t part_floats(const Shape& d, int64_t chunk) { return pad64(chunk * (d.tiles + 1) * d.G); }
 
 template <typename T, int V>
 cudaError_t fwd(const GroupNormFwd& a, Shape d, int64_t chunk, bool silu, cudaStream_t s) {
-    float2* part = (float2*)a.workspace;
+    float* part_m = (float*)a.workspace;
+    float* part_q = part_m + part_floats(d, chunk);
     constexpr size_t stage = Walk<T, V, 1, kFwdStages>::bytes;
     const size_t smem = stage + 2 * lanes_bytes(d.C, V), smem2 = stage + (size_t)d.G * 8;
     const auto apply = silu ? gn_apply_kernel<T, V, true> : gn_apply_kernel<T, V, false>;
@@ -1125,18 +1135,20 @@ cudaError_t fwd(const GroupNormFwd& a, Shape d, int64_t chunk, bool silu, cudaSt
     for (int64_t n = 0; n < a.N && e == cudaSuccess; n += chunk) {
         d.N = d2.N = std::min(chunk, a.N - n);
         const T* x = (const T*)a.x + n * d.xn;
+        float *mean = a.mean + n * d.G, *rstd = a.rstd + n * d.G;
+        float *pm = d.tiles > 1 ? part_m : mean, *pq = d.tiles > 1 ? part_q : rstd;
         e = launch(gn_stats_kernel<T, V>, dim3((unsigned)(d.N * d.tiles)), dim3(NT), smem, s, true,
-                   x, d, part);
-        const float2* p = part;
+                   x, d, pm, pq);
         if (e == cudaSuccess && d.joins < d.tiles) {
-            float2* joined = part + chunk * d.tiles * d.G;
-            e = launch(gn_join_kernel<false>, join_grid(d), dim3(NT), 0, s, true, p, joined, d);
-            p = joined;
+            float *jm = pm + chunk * d.tiles * d.G, *jq = pq + chunk * d.tiles * d.G;
+            e = launch(gn_join_kernel<false>, join_grid(d), dim3(NT), 0, s, true, (const float*)pm,
+                       (const float*)pq, jm, jq, d);
+            pm = jm, pq = jq;
         }
         if (e == cudaSuccess)
             e = launch(apply, dim3((unsigned)(d2.N * d2.tiles)), dim3(NT), smem2, s, true, x,
-                       (T*)a.y + n * d.yn, a.w, a.b, a.eps, a.mean + n * d.G, a.rstd + n * d.G, p,
-                       d2);
+                       (T*)a.y + n * d.yn, a.w, a.b, a.eps, mean, rstd, (const float*)pm,
+                       (const float*)pq, d2);
     }
     return e;
 }
@@ -1146,7 +1158,8 @@ cudaError_t bwd(const GroupNormBwd& a, Shape d, int64_t chunk, bool silu, cudaSt
     const int64_t P = grad_rows(d), chunks = a.N ? (a.N + chunk - 1) / chunk : 0;
     float* pa = (float*)a.workspace;
     float* pb = pa + pad64(chunks * P * d.C);
-    float2* pg = (float2*)(pb + pad64(chunks * P * d.C));
+    float* part_1 = pb + pad64(chunks * P * d.C);
+    float* part_2 = part_1 + part_floats(d, chunk);
     constexpr size_t stage = Walk<T, V, 2, kBwdStages>::bytes;
     const size_t smem = stage + 2 * lanes_bytes(d.C, V), smem2 = stage + (size_t)d.G * 16;
     const auto sums = silu ? gn_bwd_sums_kernel<T, V, true> : gn_bwd_sums_kernel<T, V, false>;
@@ -1161,16 +1174,18 @@ cudaError_t bwd(const GroupNormBwd& a, Shape d, int64_t chunk, bool silu, cudaSt
         const T *x = (const T*)a.x + n * d.xn, *dy = (const T*)a.dy + n * d.gn;
         const float *mean = a.mean + n * d.G, *rstd = a.rstd + n * d.G;
         e = launch(sums, dim3((unsigned)p), dim3(NT), smem, s, true, x, dy, a.w, a.b, mean, rstd, d,
-                   pg, pa + rows * d.C, pb + rows * d.C);
-        const float2* q = pg;
+                   part_1, part_2, pa + rows * d.C, pb + rows * d.C);
+        float *p1 = part_1, *p2 = part_2;
         if (e == cudaSuccess && d.joins < d.tiles) {
-            float2* joined = pg + (int64_t)chunk * d.tiles * d.G;
-            e = launch(gn_join_kernel<true>, join_grid(d), dim3(NT), 0, s, true, q, joined, d);
-            q = joined;
+            float *j1 = p1 + chunk * d.tiles * d.G, *j2 = p2 + chunk * d.tiles * d.G;
+            e = launch(gn_join_kernel<true>, join_grid(d), dim3(NT), 0, s, true, (const float*)p1,
+                       (const float*)p2, j1, j2, d);
+            p1 = j1, p2 = j2;
         }
         if (e == cudaSuccess)
             e = launch(apply, dim3((unsigned)(d.N * d.tiles)), dim3(NT), smem2, s, true, x, dy,
-                       (T*)a.dx + n * d.yn, a.w, a.b, mean, rstd, q, d);
+                       (T*)a.dx + n * d.yn, a.w, a.b, mean, rstd, (const float*)p1,
+                       (const float*)p2, d);
         rows += p;
     }
     if (e != cudaSuccess) return e;
@@ -1184,7 +1199,7 @@ int64_t groupnorm_fwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dty
     if (N == 0 || S == 0 || C == 0) return 0;
     int64_t chunk;
     const Shape d = shape_of(N, S, C, G, elt_bytes(dtype), false, chunk);
-    return part_floats(d, chunk);
+    return d.tiles > 1 ? 2 * part_floats(d, chunk) : 0;
 }
 
 int64_t groupnorm_bwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {
@@ -1192,7 +1207,7 @@ int64_t groupnorm_bwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dty
     int64_t chunk;
     const Shape d = shape_of(N, S, C, G, elt_bytes(dtype), true, chunk);
     const int64_t chunks = (N + chunk - 1) / chunk;
-    int64_t n = 2 * pad64(chunks * grad_rows(d) * C) + part_floats(d, chunk);
+    int64_t n = 2 * pad64(chunks * grad_rows(d) * C) + 2 * part_floats(d, chunk);
     RowShape r;  // taken or not by the pointers' alignment
     if (row_shape(N, S, C, G, elt_bytes(dtype), true, r)) n = std::max(n, 2 * pad64((int64_t)r.RB * C));
     return n;
