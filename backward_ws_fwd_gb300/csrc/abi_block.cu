@@ -177,7 +177,7 @@ int rotary_entry(const void* q, const int64_t* qs, void* yq, const int64_t* yqs,
 // The router's sizes and logits; *lb receives the span of [T, E] at stride ld.
 int router_sizes(int64_t T, int64_t E, int64_t k, int64_t ld, int es, int64_t* lb) {
     if (T < 0 || E < 1 || E > wsf::kRouterMaxE || k < 1 || k > E || k > wsf::kRouterMaxK ||
-        T > INT32_MAX / k)
+        T > INT32_MAX / k || T > wsf::kRouterMaxT)
         return WSF_ERR_BAD_SHAPE;
     *lb = 0;
     if (T == 0) return WSF_OK;
@@ -235,7 +235,7 @@ int rotary_bwd(const void* dyq, const int64_t* dyq_strides, void* dq, const int6
 }
 
 size_t router_fwd_workspace_bytes(int64_t T, int64_t E) {
-    if (T < 0 || E < 1 || E > wsf::kRouterMaxE) return SIZE_MAX;
+    if (T < 0 || T > wsf::kRouterMaxT || E < 1 || E > wsf::kRouterMaxE) return SIZE_MAX;
     const int64_t P = wsf::router_tiles(T, E);  // one block joins its sums itself
     return P > 1 ? (size_t)(P * E * 8) : 0;
 }

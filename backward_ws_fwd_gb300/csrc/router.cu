@@ -329,20 +329,24 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
 
     // (rows fit an int: T·k < 2³¹; rows behind the last read the last one)
     const int step = gridDim.x * NW * RPW;
+    int row = (int)(blockIdx.x * NW + wid) * RPW + grp;
+    const T* src = (const T*)a.logits + (int64_t)min(row, T_ - 1) * a.ld;
+    const int64_t jump = (int64_t)step * a.ld;
+    float* gates = a.gates + (int64_t)row * k;
+    int* ids = a.ids + (int64_t)row * k;
     Logits<T, L, R> next;
     unsigned char keep = 1;
-    auto ask = [&](int64_t r) {
-        const int64_t q = r < T_ ? r : T_ - 1;
-        next.load((const T*)a.logits + q * a.ld, sub, E, a.vec);
-        if (a.mask) keep = __ldg(a.mask + q);
-    };
-    int64_t row = (int)(blockIdx.x * NW + wid) * RPW + grp;
-    if (row - grp < T_) ask(row);
-    for (; row - grp < T_; row += step) {
+    next.load(src, sub, E, a.vec);
+    if (a.mask) keep = __ldg(a.mask + min(row, T_ - 1));
+    for (; row - grp < T_; row += step, gates += step * k, ids += step * k) {
         Logits<T, L, R> x = next;
         x.end(sub, E);
         bool valid = keep && row < T_;
-        if (row - grp + step < T_) ask(row + step);  // in flight meanwhile
+        if (row + step < T_) {  // in flight meanwhile
+            src += jump;
+            next.load(src, sub, E, a.vec);
+            if (a.mask) keep = __ldg(a.mask + row + step);
+        }
 
         // the k largest, in order: every lane sorts its runs and offers the
         // first of what is left of them
@@ -414,9 +418,8 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
         if (row < T_) {
             for (int j = sub; j < k; j += L) {
                 const P q = mine[j];
-                const int to = (int)row * k + j;
-                a.gates[to] = valid ? exp_of(key_value<T>(q.key), m) * inv : 0.f;
-                a.ids[to] = valid ? q.id() : -1;
+                gates[j] = valid ? exp_of(key_value<T>(q.key), m) * inv : 0.f;
+                ids[j] = valid ? q.id() : -1;
                 if (valid) atomicAdd(&cnt[q.id()], 1);
             }
         }
@@ -624,26 +627,33 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
     Logits<T, L, R> next;
     int next_id = -1;
     float next_dg = 0.f;
-    auto ask = [&](int64_t r) {
-        const int64_t q = r < T_ ? r : T_ - 1;
-        next.load((const T*)a.logits + q * a.ld, sub, E, a.vec);
-        next_id = -1;
-        if (r < T_ && sub < k) {
-            next_id = __ldg(a.ids + q * k + sub);
-            if (a.dgates) next_dg = __ldg(a.dgates + q * k + sub);
-        }
-    };
-    int64_t row = (int)(blockIdx.x * NW + wid) * RPW + grp;
-    if (row - grp < T_) ask(row);
-    for (; row - grp < T_; row += step) {
+    int row = (int)(blockIdx.x * NW + wid) * RPW + grp;
+    const T* ahead = (const T*)a.logits + (int64_t)min(row, T_ - 1) * a.ld;
+    const int64_t jump = (int64_t)step * a.ld;
+    const int* ids = a.ids + (int64_t)min(row, T_ - 1) * k;  // of the row
+    const float* dg = a.dgates + (int64_t)min(row, T_ - 1) * k;
+    T* out_row = (T*)a.dlogits + (int64_t)row * a.ldd;
+    next.load(ahead, sub, E, a.vec);
+    if (row < T_ && sub < k) {
+        next_id = __ldg(ids + sub);
+        if (a.dgates) next_dg = __ldg(dg + sub);
+    }
+    for (; row - grp < T_; row += step, ids += step * k, dg += step * k,
+                           out_row += (int64_t)step * a.ldd) {
         Logits<T, L, R> x = next;
         x.end(sub, E);
         const int id0 = next_id;
         const float dg0 = next_dg;
-        if (row - grp + step < T_) ask(row + step);
-        const T* src = (const T*)a.logits + row * a.ld;
-        const int* ids = a.ids + row * k;
-        const float* dg = a.dgates + row * k;
+        const T* src = ahead;
+        next_id = -1;
+        if (row + step < T_) {
+            ahead += jump;
+            next.load(ahead, sub, E, a.vec);
+            if (sub < k) {
+                next_id = __ldg(ids + step * k + sub);
+                if (a.dgates) next_dg = __ldg(dg + step * k + sub);
+            }
+        }
         const bool valid = __shfl_sync(FULL_MASK, id0, lane & ~(L - 1)) >= 0;
         const bool put_u = valid && a.dgates, put0 = put_u && (unsigned)id0 < (unsigned)E;
 
@@ -742,7 +752,7 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < EPL; i++) out[i] = 0.f;
         }
-        if (row < T_) store_row<T, L, R>((T*)a.dlogits + row * a.ldd, sub, E, a.vec, out);
+        if (row < T_) store_row<T, L, R>(out_row, sub, E, a.vec, out);
         __syncwarp();
     }
     pdl_trigger();

@@ -29,7 +29,8 @@ cudaError_t launch_rotary(const RotaryHeads& q, const RotaryHeads& k, const void
 
 // Top-k router.  router_tiles: rows P of the forward's partial sums
 // (workspace, for P > 1: P·E floats, then P·E ints).
-constexpr int64_t kRouterMaxE = 1024, kRouterMaxK = 32;
+// (Row numbers run one turn of the grid past T in an int.)
+constexpr int64_t kRouterMaxE = 1024, kRouterMaxK = 32, kRouterMaxT = 1 << 30;
 int64_t router_tiles(int64_t T, int64_t E);
 cudaError_t launch_router_fwd(const void* logits, int64_t ld, const unsigned char* mask, int64_t k,
                               int renorm, float* gates, int* ids, int* counts, float* loss,

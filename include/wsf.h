@@ -354,7 +354,7 @@ int rotary_bwd(const void* dyq, const int64_t* dyq_strides, void* dq, const int6
  * and the loss NaN; its ids are k different experts.
  * gates: [T, k] binary32, ids: [T, k] int32, counts: [E] int32, loss: one
  * binary32, all contiguous.  1 <= k <= min(E, 32), 1 <= E <= 1024,
- * T·k < 2^31 (WSF_ERR_BAD_SHAPE).  workspace: router_fwd_workspace_bytes
+ * T <= 2^30, T·k < 2^31 (WSF_ERR_BAD_SHAPE).  workspace: router_fwd_workspace_bytes
  * bytes (per-block partial sums, joined in a fixed order: the same bits on every run).
  */
 size_t router_fwd_workspace_bytes(int64_t T, int64_t E);

@@ -94,7 +94,7 @@ def test_router_fwd_rejects(wsf):
     r = lambda **o: router_fwd(wsf, **o)  # noqa: E731
     assert r(dt=3) == wsf.ERR_BAD_DTYPE
     for o in (dict(T=-1), dict(E=0), dict(E=1025, ld=2000), dict(k=0), dict(k=33), dict(E=4, k=5),
-              dict(T=1 << 30), dict(ld=1 << 60)):
+              dict(T=1 << 30), dict(T=(1 << 30) + 1, k=1), dict(ld=1 << 60)):
         assert r(**o) == wsf.ERR_BAD_SHAPE, o
     assert r(renorm=2) == wsf.ERR_BAD_ARG
     assert r(ld=63) == wsf.ERR_BAD_STRIDE
