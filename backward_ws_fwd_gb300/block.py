@@ -7,6 +7,7 @@ checked here (TypeError, ValueError); the rest is checked there (WsfError).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 from . import SIZE_MAX, _check, _dtype_code, _scratch, lib
@@ -72,13 +73,13 @@ def _like(t, name, x):
         _refuse(t, name, x.dtype, x.shape, x.device)
 
 
-def _launch(call, what, t, stream, *args):
-    """call(*args, stream) with t's device current."""
+def _launch(call, what, t, *args):
+    """call(*args, stream) on the current stream of t's device."""
     import torch
     dev = t.get_device()
     if dev < 0:  # host memory, which the library cannot tell from the device's
         raise ValueError(f"{what}: the tensors are not on a GPU")
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    raw = torch._C._cuda_getCurrentRawStream(dev)
     if torch.cuda.current_device() == dev:
         rc = call(*args, raw)
     else:
@@ -88,17 +89,35 @@ def _launch(call, what, t, stream, *args):
         _check(rc, what)
 
 
+def _on_stream(fn):
+    """Give fn a `stream` argument: the call is made with that stream current,
+    so that what it allocates (results and temporary workspaces) belongs to the
+    stream that writes it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        t = next(a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor))
+        if t.device != stream.device:
+            raise ValueError(f"the tensors are on {t.device}, the stream on {stream.device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    return call
+
+
 def _p(t):
     """Address of t's data, None where it has none."""
     return t.data_ptr() if t is not None and t.numel() else None
 
 
-def _work(need, workspace, t, stream):
+def _work(need, workspace, t):
     """(address, bytes, tensor) of the caller's workspace, or of a temporary one."""
     if workspace is None:
         if need == 0 or need == SIZE_MAX:
             return None, 0, None
-        workspace = _scratch(need, t.device, stream)
+        workspace = _scratch(need, t.device, None)
     return _p(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -110,7 +129,7 @@ def _strides3(t):
     return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
-def _rotary(call, what, q, k, positions, inv_freq, scale, interleaved, q_out, k_out, stream):
+def _rotary(call, what, q, k, positions, inv_freq, scale, interleaved, q_out, k_out):
     import torch
     shape = q.shape
     if len(shape) == 4:
@@ -160,7 +179,7 @@ def _rotary(call, what, q, k, positions, inv_freq, scale, interleaved, q_out, k_
         _refuse(positions, "positions", None, None, dev)
     strides = _st12(*sq, *so, *sk, *sp)  # read before the call returns
     at = ctypes.addressof(strides)
-    _launch(call, what, q, stream, _p(q), at, _p(q_out), at + 24, H, _p(k), at + 48, _p(k_out),
+    _launch(call, what, q, _p(q), at, _p(q_out), at + 24, H, _p(k), at + 48, _p(k_out),
             at + 72, Hk, _p(positions), ldp, pb, _p(inv_freq), scale, 1 if interleaved else 0, B,
             S, D, R, code)
     return q_out, k_out
@@ -169,22 +188,22 @@ def _rotary(call, what, q, k, positions, inv_freq, scale, interleaved, q_out, k_
 _NONE3 = (0, 0, 0)
 
 
-def rotary_fwd(q, k, positions, inv_freq, scale=1.0, interleaved=False, q_out=None, k_out=None,
-               stream=None):
+@_on_stream
+def rotary_fwd(q, k, positions, inv_freq, scale=1.0, interleaved=False, q_out=None, k_out=None):
     """Rotary positions of q [B, S, Hq, D] (or [T, Hq, D]) and k (Hk heads, or
     None), any layout of unit inner stride.  positions: int32 or int64 [B, S],
     [S] or [T]; inv_freq: float32 [R/2] (see rotary_frequencies), the first R
     elements of a head are rotated, the others copied.  scale multiplies cos
     and sin.  q_out=q, k_out=k rotates in place.  Returns (yq, yk)."""
     return _rotary(lib.rotary_fwd, "rotary_fwd", q, k, positions, inv_freq, scale, interleaved,
-                   q_out, k_out, stream)
+                   q_out, k_out)
 
 
-def rotary_bwd(dyq, dyk, positions, inv_freq, scale=1.0, interleaved=False, dq=None, dk=None,
-               stream=None):
+@_on_stream
+def rotary_bwd(dyq, dyk, positions, inv_freq, scale=1.0, interleaved=False, dq=None, dk=None):
     """The vector-Jacobian product of rotary_fwd: (dq, dk) from (dyq, dyk)."""
     return _rotary(lib.rotary_bwd, "rotary_bwd", dyq, dyk, positions, inv_freq, scale, interleaved,
-                   dq, dk, stream)
+                   dq, dk)
 
 
 def rotary_frequencies(R, base=10000.0, scaling=None, factor=1.0, original_length=None, fast=32.0,
@@ -236,8 +255,9 @@ def router_fwd_workspace_bytes(T: int, E: int) -> int:
     return lib.router_fwd_workspace_bytes(T, E)
 
 
+@_on_stream
 def router_fwd(logits, k, mask=None, renormalize=False, gates=None, ids=None, counts=None,
-               loss=None, workspace=None, stream=None):
+               loss=None, workspace=None):
     """Top-k routing with the balance loss.  logits: [T, E] (unit inner
     stride); mask: bool or uint8 [T], False leaves a row out.  Returns (gates
     float32 [T, k], ids int32 [T, k], counts int32 [E], loss float32 [])."""
@@ -265,14 +285,15 @@ def router_fwd(logits, k, mask=None, renormalize=False, gates=None, ids=None, co
         loss = torch.empty((), dtype=torch.float32, device=dev)
     else:
         _want(loss, "loss", torch.float32, (), dev)
-    ws, wbytes, keep = _work(lib.router_fwd_workspace_bytes(T, E), workspace, logits, stream)
-    _launch(lib.router_fwd, "router_fwd", logits, stream, _p(logits), logits.stride(0), _p(mask),
+    ws, wbytes, keep = _work(lib.router_fwd_workspace_bytes(T, E), workspace, logits)
+    _launch(lib.router_fwd, "router_fwd", logits, _p(logits), logits.stride(0), _p(mask),
             k, 1 if renormalize else 0, _p(gates), _p(ids), _p(counts), _p(loss), ws, wbytes, T, E,
             code)
     return gates, ids, counts, loss
 
 
-def router_bwd(logits, ids, counts, dgates, dloss, renormalize=False, dlogits=None, stream=None):
+@_on_stream
+def router_bwd(logits, ids, counts, dgates, dloss, renormalize=False, dlogits=None):
     """dlogits of router_fwd from ids and counts as it returned them, dgates
     (float32 [T, k] or None) and dloss (float32 [] or None)."""
     import torch
@@ -291,7 +312,7 @@ def router_bwd(logits, ids, counts, dgates, dloss, renormalize=False, dlogits=No
         dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
     else:
         _like(dlogits, "dlogits", logits)
-    _launch(lib.router_bwd, "router_bwd", logits, stream, _p(logits), logits.stride(0), _p(ids),
+    _launch(lib.router_bwd, "router_bwd", logits, _p(logits), logits.stride(0), _p(ids),
             _p(counts), k, 1 if renormalize else 0, _p(dgates), _p(dloss), _p(dlogits),
             dlogits.stride(0), T, E, code)
     return dlogits
@@ -332,8 +353,9 @@ def _act(act):
         raise ValueError(f"unknown activation {act!r}") from None
 
 
+@_on_stream
 def groupnorm_fwd(x, w, b, groups, eps=1e-5, act=None, y=None, mean=None, rstd=None,
-                  workspace=None, stream=None):
+                  workspace=None):
     """Group norm of x [N, S, C] (or [N, C], S = 1), channels last, over
     `groups` groups of consecutive channels; w, b: float32 [C]; act: None or
     "silu".  Returns (y, mean, rstd), the statistics float32 [N, groups]."""
@@ -355,16 +377,16 @@ def groupnorm_fwd(x, w, b, groups, eps=1e-5, act=None, y=None, mean=None, rstd=N
         rstd = torch.empty((N, groups), dtype=torch.float32, device=dev)
     else:
         _want(rstd, "rstd", torch.float32, (N, groups), dev)
-    ws, wbytes, keep = _work(lib.groupnorm_fwd_workspace_bytes(N, S, C, groups, code), workspace, x,
-                             stream)
-    _launch(lib.groupnorm_fwd, "groupnorm_fwd", x, stream, _p(x), *_ns_strides(x), _p(w), _p(b),
+    ws, wbytes, keep = _work(lib.groupnorm_fwd_workspace_bytes(N, S, C, groups, code), workspace, x)
+    _launch(lib.groupnorm_fwd, "groupnorm_fwd", x, _p(x), *_ns_strides(x), _p(w), _p(b),
             eps, act, _p(y), *_ns_strides(y), _p(mean), _p(rstd), ws, wbytes, N, S, C, groups,
             code)
     return y, mean, rstd
 
 
+@_on_stream
 def groupnorm_bwd(x, w, b, mean, rstd, dy, groups, act=None, dx=None, grad_w=None, grad_b=None,
-                  accumulate=False, workspace=None, stream=None):
+                  accumulate=False, workspace=None):
     """dx, grad_w (+)= Σ dz·x̂ and grad_b (+)= Σ dz of groupnorm_fwd, from its
     statistics.  Returns (dx, grad_w, grad_b)."""
     import torch
@@ -388,9 +410,8 @@ def groupnorm_bwd(x, w, b, mean, rstd, dy, groups, act=None, dx=None, grad_w=Non
         grad_b = torch.empty(C, dtype=torch.float32, device=dev)
     else:
         _want(grad_b, "grad_b", torch.float32, (C,), dev)
-    ws, wbytes, keep = _work(lib.groupnorm_bwd_workspace_bytes(N, S, C, groups, code), workspace, x,
-                             stream)
-    _launch(lib.groupnorm_bwd, "groupnorm_bwd", x, stream, _p(x), *_ns_strides(x), _p(w), _p(b),
+    ws, wbytes, keep = _work(lib.groupnorm_bwd_workspace_bytes(N, S, C, groups, code), workspace, x)
+    _launch(lib.groupnorm_bwd, "groupnorm_bwd", x, _p(x), *_ns_strides(x), _p(w), _p(b),
             _p(mean), _p(rstd), _p(dy), *_ns_strides(dy), act, _p(dx), *_ns_strides(dx),
             _p(grad_w), _p(grad_b), 1 if accumulate else 0, ws, wbytes, N, S, C, groups, code)
     return dx, grad_w, grad_b

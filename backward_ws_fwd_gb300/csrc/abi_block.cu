@@ -200,7 +200,9 @@ bool clash(const Span* outs, int no, const Span* ins, int ni) {
 }
 
 bool groupnorm_sizes(int64_t N, int64_t S, int64_t C, int64_t G) {
-    if (N < 0 || S < 0 || C < 0 || G < 1 || C > wsf::kGroupNormMaxC || C % G) return false;
+    if (N < 0 || S < 0 || C < 0 || G < 1 || C > wsf::kGroupNormMaxC ||
+        G > wsf::kGroupNormMaxG || S > wsf::kGroupNormMaxS || C % G)
+        return false;
     // sizes and workspaces in bytes stay inside int64
     if (C == 0 || N == 0 || S == 0) return N <= INT32_MAX;
     return N <= INT32_MAX / G && S <= (INT64_MAX / 4096) / C / N;

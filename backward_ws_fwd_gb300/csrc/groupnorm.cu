@@ -496,9 +496,9 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(const float* pm, const floa
 }
 
 // Second pass.  The block first joins its sample's partial statistics, lg
-// lanes a group; the first tile's block writes the statistics out.  (Samples of
-// one tile keep their partial statistics where the results go: the one block
-// that reads them replaces them.)
+// lanes a group; the first tile's block writes the statistics out.  (Samples
+// that are one tile in both passes keep their partial statistics where the
+// results go: the one block that reads them replaces them.)
 template <typename T, int V, bool Silu>
 __global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T* y, const float* w,
                                                       const float* b, float eps, float* mean,
@@ -1120,6 +1120,12 @@ dim3 join_grid(const Shape& d) { return dim3((unsigned)((d.N * d.G + NT / 32 - 1
 // One plane of the partial statistics of a chunk's tiles, and of its samples.
 int64_t part_floats(const Shape& d, int64_t chunk) { return pad64(chunk * (d.tiles + 1) * d.G); }
 
+// The forward's second pass has tiles of its own.
+Shape second_tiles(Shape d, int64_t chunk, int es) {
+    tile(d, chunk, kDesignSMs * kApplyCtas, es);
+    return d;
+}
+
 template <typename T, int V>
 cudaError_t fwd(const GroupNormFwd& a, Shape d, int64_t chunk, bool silu, cudaStream_t s) {
     float* part_m = (float*)a.workspace;
@@ -1130,13 +1136,14 @@ cudaError_t fwd(const GroupNormFwd& a, Shape d, int64_t chunk, bool silu, cudaSt
     cudaError_t e = allow(gn_stats_kernel<T, V>, smem);
     if (e == cudaSuccess) e = allow(apply, smem2);
     steps(d, V);
-    Shape d2 = d;
-    tile(d2, chunk, kDesignSMs * kApplyCtas, (int)sizeof(T));
+    const Shape t2 = second_tiles(d, chunk, (int)sizeof(T));
+    const bool whole = d.tiles == 1 && t2.tiles == 1;
+    Shape d2 = t2;
     for (int64_t n = 0; n < a.N && e == cudaSuccess; n += chunk) {
         d.N = d2.N = std::min(chunk, a.N - n);
         const T* x = (const T*)a.x + n * d.xn;
         float *mean = a.mean + n * d.G, *rstd = a.rstd + n * d.G;
-        float *pm = d.tiles > 1 ? part_m : mean, *pq = d.tiles > 1 ? part_q : rstd;
+        float *pm = whole ? mean : part_m, *pq = whole ? rstd : part_q;
         e = launch(gn_stats_kernel<T, V>, dim3((unsigned)(d.N * d.tiles)), dim3(NT), smem, s, true,
                    x, d, pm, pq);
         if (e == cudaSuccess && d.joins < d.tiles) {
@@ -1199,7 +1206,8 @@ int64_t groupnorm_fwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dty
     if (N == 0 || S == 0 || C == 0) return 0;
     int64_t chunk;
     const Shape d = shape_of(N, S, C, G, elt_bytes(dtype), false, chunk);
-    return d.tiles > 1 ? 2 * part_floats(d, chunk) : 0;
+    const bool whole = d.tiles == 1 && second_tiles(d, chunk, elt_bytes(dtype)).tiles == 1;
+    return whole ? 0 : 2 * part_floats(d, chunk);
 }
 
 int64_t groupnorm_bwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dtype) {

@@ -41,7 +41,7 @@ cudaError_t launch_router_bwd(const void* logits, int64_t ld, const int* ids, co
                               cudaStream_t s);
 
 // Group norm of [N, S, C]; strides in elements.  *_floats: workspace size.
-constexpr int64_t kGroupNormMaxC = 16384;
+constexpr int64_t kGroupNormMaxC = 16384, kGroupNormMaxG = 8192, kGroupNormMaxS = 1ll << 38;
 struct GroupNormFwd {
     const void* x;
     int64_t x_n, x_s;

@@ -389,7 +389,8 @@ int router_bwd(const void* logits, int64_t ld, const int* ids, const int* counts
  * S == 1 is the norm of a token's heads; S = H·W that of feature maps.
  * x, y, dy, dx: dtype, unit stride along C, strides x_n (sample) and x_s
  * (row, >= C) in elements.  w, b, grad_w, grad_b: [C] binary32.
- * C <= 16384, C % G == 0 (WSF_ERR_BAD_SHAPE), eps finite and >= 0.  The
+ * C <= 16384, G <= 8192, C % G == 0, S <= 2^38 (WSF_ERR_BAD_SHAPE), eps
+ * finite and >= 0; workspace 8-byte aligned.  The
  * statistics are kept for the backward, which would otherwise read x once
  * more than it has to (a group does not fit one block, unlike a row of
  * layernorm_bwd); arithmetic is binary32, each output rounded once.

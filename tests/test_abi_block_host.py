@@ -147,7 +147,8 @@ def test_groupnorm_fwd_rejects(wsf):
     r = lambda **o: gn_fwd(wsf, **o)  # noqa: E731
     assert r(dt=4) == wsf.ERR_BAD_DTYPE
     for o in (dict(N=-1), dict(S=-1), dict(C=-320), dict(G=0), dict(G=-1), dict(G=33),
-              dict(C=16416, G=32), dict(N=1 << 40), dict(S=1 << 55), dict(xn=1 << 62)):
+              dict(C=16416, G=32), dict(C=16384, G=16384, xs=16384, ys=16384),
+              dict(S=(1 << 38) + 1), dict(N=1 << 40), dict(S=1 << 55), dict(xn=1 << 62)):
         assert r(**o) == wsf.ERR_BAD_SHAPE, o
     for o in (dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(act=2), dict(act=-1)):
         assert r(**o) == wsf.ERR_BAD_ARG, o

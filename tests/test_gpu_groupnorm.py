@@ -117,6 +117,17 @@ def test_offsets_outliers_and_constants(wsf, dtype, N, S, C, G):
     _check(wsf, flat.to(dtype), w, b, dy.to(dtype), G, "silu")
 
 
+def test_samples_whose_passes_are_tiled_differently(wsf):
+    """Numbers of samples for which the second pass cuts a sample into more
+    tiles than the first."""
+    for N in (153, 200, 228, 304, 305, 456, 457):
+        x, w, b, dy = _inputs(N, 300, 64, torch.float32, N)
+        for _ in range(3):
+            y, mean, rstd = wsf.groupnorm_fwd(x, w, b, 4, EPS, "silu")
+        r = ref.groupnorm(x, w, b, 4, EPS, True)
+        _compare(dict(y=y, mean=mean, rstd=rstd), r)
+
+
 def test_special_values_stay_in_their_group(wsf):
     for N, S, C, G in ((6, 1, 512, 4), (3, 50, 64, 8)):
         x, w, b, dy = _inputs(N, S, C, torch.bfloat16, 7)
@@ -213,6 +224,34 @@ def test_large_offsets(wsf):
     d = wsf.groupnorm_bwd(x, w, b, mean, rstd, dy, G, "silu")
     for p, q in zip(d, wsf.groupnorm_bwd(x0, w, b, mean, rstd, dy, G, "silu")):
         assert torch.equal(p, q)
+
+
+def test_many_groups(wsf):
+    """One channel a group, as many groups as there may be."""
+    x, w, b, dy = _inputs(2, 5, 8192, torch.bfloat16, 15)
+    _check(wsf, x, w, b, dy, 8192, "silu")
+
+
+def test_allocates_on_the_given_stream(wsf):
+    """What a call on another stream allocates is not memory that the current
+    stream still uses: a long chain of work there keeps its result."""
+    x, w, b, dy = _inputs(64, 400, 64, torch.bfloat16, 16)
+    want = wsf.groupnorm_fwd(x, w, b, 4, EPS, "silu")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        a = torch.full_like(x, 3.0)
+        for _ in range(20):
+            a.mul_(1.0)  # still running when a's memory is given back
+        total = a.float().sum()
+        del a
+        got = wsf.groupnorm_fwd(x, w, b, 4, EPS, "silu", stream=s)
+        s.synchronize()
+        assert float(total) == 3.0 * x.numel()
+        for p, q in zip(got, want):
+            assert torch.equal(p, q)
+    with pytest.raises(TypeError):
+        wsf.groupnorm_fwd(x, w, b, 4, EPS, "silu", None, None, None, None, s)
 
 
 def test_streams_and_graphs(wsf):
