@@ -84,17 +84,18 @@ __device__ __forceinline__ int expert(int i, int sub) {
 
 // A lane's 8·R logits of a row as they are stored (8 of a 16-bit type in 4
 // words, of binary32 in 8), −inf behind the last expert.  Rows of experts in
-// eights at 16-byte addresses (vec) are read and written 16 bytes at a time,
-// others element by element.
-template <typename T, int L, int R>
+// eights at 16-byte addresses (Vec) are read and written 16 bytes at a time,
+// others element by element; a kernel of its own for each, since a branch
+// between them would be compiled into predicated instructions of both.
+template <typename T, int L, int R, bool Vec>
 struct Logits {
     static constexpr int W = 8 * (int)sizeof(T) / 4;  // words of a run
     uint32_t w[R * W];
 
     // What lies behind the last expert is put right by end(), when the row's
     // turn comes: touching the words here would wait for the load.
-    __device__ __forceinline__ void load(const T* row, int sub, int E, bool vec) {
-        if (vec) {
+    __device__ __forceinline__ void load(const T* row, int sub, int E) {
+        if constexpr (Vec) {
 #pragma unroll
             for (int r = 0; r < R; r++) {
                 const int e0 = expert<L>(r * 8, sub), at = e0 < E ? e0 : 0;
@@ -118,19 +119,24 @@ struct Logits {
             }
         }
     }
+    // Whether element i lies behind the last expert (Vec: with its whole run).
+    __device__ __forceinline__ static bool past(int i, int sub, int E) {
+        return expert<L>(Vec ? i / 8 * 8 : i, sub) >= E;
+    }
     __device__ __forceinline__ void end(int sub, int E) {
-        if (E == 8 * R * L) return;
         constexpr uint32_t none = sizeof(T) == 4                     ? 0xff800000u
                                   : std::is_same<T, __half>::value ? 0xfc00u
                                                                    : 0xff80u;
+        if constexpr (Vec || sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8 * R; i++) {
-            const bool past = expert<L>(i, sub) >= E;
-            if constexpr (sizeof(T) == 4) {
-                w[i] = past ? none : w[i];
-            } else {
+            for (int i = 0; i < R * W; i++)
+                if (past(i * 8 / W, sub, E)) w[i] = sizeof(T) == 4 ? none : none * 0x10001u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8 * R; i++) {
                 uint32_t& d = w[i / 2];
-                d = past ? (i & 1 ? (d & 0xffffu) | none << 16 : (d & 0xffff0000u) | none) : d;
+                if (past(i, sub, E))
+                    d = i & 1 ? (d & 0xffffu) | none << 16 : (d & 0xffff0000u) | none;
             }
         }
     }
@@ -181,10 +187,11 @@ struct Logits {
                 key[2 * i + 1] = (b & 0xffff0000u) | (c - 1u);
             }
         }
-        if (E < 8 * R * L) {
+        // (a run that lies behind as a whole is left out by its head)
+        if constexpr (!Vec) {
 #pragma unroll
             for (int i = 0; i < 8 * R; i++)
-                if (expert<L>(i, sub) >= E) key[i] = 0u;
+                if (past(i, sub, E)) key[i] = 0u;
         }
     }
 };
@@ -286,7 +293,7 @@ struct FwdArgs {
     float* loss;
     int64_t ld;
     int T;
-    int E, k, renorm, vec;
+    int E, k, renorm;
 };
 
 // E·Σ c·S / (k·V²) with V = chose / k rows that count.
@@ -303,7 +310,7 @@ size_t fwd_smem(int k) {
            (size_t)L * 8 * R * 4;
 }
 
-template <typename T, int L, int R>
+template <typename T, int L, int R, bool Vec>
 __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
     router_fwd_kernel(const FwdArgs a) {
     using P = Pick<T>;
@@ -334,17 +341,17 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
     const int64_t jump = (int64_t)step * a.ld;
     float* gates = a.gates + (int64_t)row * k;
     int* ids = a.ids + (int64_t)row * k;
-    Logits<T, L, R> next;
+    Logits<T, L, R, Vec> next;
     unsigned char keep = 1;
-    next.load(src, sub, E, a.vec);
+    next.load(src, sub, E);
     if (a.mask) keep = __ldg(a.mask + min(row, T_ - 1));
     for (; row - grp < T_; row += step, gates += step * k, ids += step * k) {
-        Logits<T, L, R> x = next;
+        Logits<T, L, R, Vec> x = next;
         x.end(sub, E);
         bool valid = keep && row < T_;
         if (row + step < T_) {  // in flight meanwhile
             src += jump;
-            next.load(src, sub, E, a.vec);
+            next.load(src, sub, E);
             if (a.mask) keep = __ldg(a.mask + row + step);
         }
 
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
 #pragma unroll
             for (int q = 0; q < 8; q++) s[q] = P::of(key[r * 8 + q], expert<L>(r * 8 + q, sub));
             sort8(s);
-            head[r] = s[0];
+            head[r] = Vec && x.past(r * 8, sub, E) ? P::of(0u, -1) : s[0];
 #pragma unroll
             for (int q = 1; q < 8; q++) run[(r * 9 + q) * 32] = s[q];
         }
@@ -557,17 +564,16 @@ struct BwdArgs {
     void* dlogits;
     int64_t ld, ldd;
     int T;
-    int E, k, renorm, vec;
+    int E, k, renorm;
 };
 
-template <typename T, int L, int R>
-__device__ __forceinline__ void store_row(T* row, int sub, int E, bool vec,
-                                          const float (&f)[8 * R]) {
+template <typename T, int L, int R, bool Vec>
+__device__ __forceinline__ void store_row(T* row, int sub, int E, const float (&f)[8 * R]) {
     constexpr int V = Elt<T>::V;
 #pragma unroll
     for (int r = 0; r < R; r++) {
         const int e0 = expert<L>(r * 8, sub);
-        if (vec) {
+        if constexpr (Vec) {
 #pragma unroll
             for (int h = 0; h < 8; h += V) {
                 float g[V];
@@ -588,7 +594,7 @@ size_t bwd_smem() {
     return (size_t)NW * 32 * 8 * R * 4 + 64;
 }
 
-template <typename T, int L, int R, bool Renorm>
+template <typename T, int L, int R, bool Vec, bool Renorm>
 __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
     router_bwd_kernel(const BwdArgs a) {
     constexpr int EPL = 8 * R, RPW = 32 / L, SLOTS = L * EPL;
@@ -624,7 +630,7 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
     const int step = gridDim.x * NW * RPW, T_ = a.T;
     const bool few = k <= L;  // one choice a lane
     // a row, and the lane's first choice of it, a turn ahead
-    Logits<T, L, R> next;
+    Logits<T, L, R, Vec> next;
     int next_id = -1;
     float next_dg = 0.f;
     int row = (int)(blockIdx.x * NW + wid) * RPW + grp;
@@ -633,14 +639,14 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
     const int* ids = a.ids + (int64_t)min(row, T_ - 1) * k;  // of the row
     const float* dg = a.dgates + (int64_t)min(row, T_ - 1) * k;
     T* out_row = (T*)a.dlogits + (int64_t)row * a.ldd;
-    next.load(ahead, sub, E, a.vec);
+    next.load(ahead, sub, E);
     if (row < T_ && sub < k) {
         next_id = __ldg(ids + sub);
         if (a.dgates) next_dg = __ldg(dg + sub);
     }
     for (; row - grp < T_; row += step, ids += step * k, dg += step * k,
                            out_row += (int64_t)step * a.ldd) {
-        Logits<T, L, R> x = next;
+        Logits<T, L, R, Vec> x = next;
         x.end(sub, E);
         const int id0 = next_id;
         const float dg0 = next_dg;
@@ -648,7 +654,7 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
         next_id = -1;
         if (row + step < T_) {
             ahead += jump;
-            next.load(ahead, sub, E, a.vec);
+            next.load(ahead, sub, E);
             if (sub < k) {
                 next_id = __ldg(ids + step * k + sub);
                 if (a.dgates) next_dg = __ldg(dg + step * k + sub);
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < EPL; i++) out[i] = 0.f;
         }
-        if (row < T_) store_row<T, L, R>(out_row, sub, E, a.vec, out);
+        if (row < T_) store_row<T, L, R, Vec>(out_row, sub, E, out);
         __syncwarp();
     }
     pdl_trigger();
@@ -771,34 +777,35 @@ int64_t blocks_for(int64_t T, int64_t E, bool backward) {
     return b < 1 ? 1 : b > most ? most : b;
 }
 
-template <typename T, int L, int R>
+template <typename T, int L, int R, bool Vec>
 cudaError_t run_fwd(const FwdArgs& a, int64_t P, cudaStream_t s) {
+    const auto k = router_fwd_kernel<T, L, R, Vec>;
     const size_t smem = fwd_smem<T, L, R>(a.k);
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute((const void*)router_fwd_kernel<T, L, R>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(
+            (const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch(router_fwd_kernel<T, L, R>, dim3((unsigned)P), dim3(NT), smem, s, true, a);
+    return launch(k, dim3((unsigned)P), dim3(NT), smem, s, true, a);
 }
-template <typename T, int L, int R>
+template <typename T, int L, int R, bool Vec>
 cudaError_t run_bwd(const BwdArgs& a, int64_t P, cudaStream_t s) {
-    return launch(a.renorm ? router_bwd_kernel<T, L, R, true> : router_bwd_kernel<T, L, R, false>,
-                  dim3((unsigned)P), dim3(NT), bwd_smem<L, R>(), s,
-                  true, a);
+    return launch(a.renorm ? router_bwd_kernel<T, L, R, Vec, true>
+                           : router_bwd_kernel<T, L, R, Vec, false>,
+                  dim3((unsigned)P), dim3(NT), bwd_smem<L, R>(), s, true, a);
 }
 
 // The lanes of a row follow from the number of experts alone.
-#define ROUTER_BY_E(RUN, T)                             \
-    (a.E <= 8     ? RUN<T, 1, 1>(a, P, s)               \
-     : a.E <= 16  ? RUN<T, 2, 1>(a, P, s)               \
-     : a.E <= 32  ? RUN<T, 4, 1>(a, P, s)               \
-     : a.E <= 64  ? RUN<T, 8, 1>(a, P, s)               \
-     : a.E <= 128 ? RUN<T, 16, 1>(a, P, s)              \
-     : a.E <= 256 ? RUN<T, 32, 1>(a, P, s)              \
-     : a.E <= 512 ? RUN<T, 32, 2>(a, P, s)              \
-                  : RUN<T, 32, 4>(a, P, s))
+#define ROUTER_BY_E(RUN, T, VEC)                        \
+    (a.E <= 8     ? RUN<T, 1, 1, VEC>(a, P, s)          \
+     : a.E <= 16  ? RUN<T, 2, 1, VEC>(a, P, s)          \
+     : a.E <= 32  ? RUN<T, 4, 1, VEC>(a, P, s)          \
+     : a.E <= 64  ? RUN<T, 8, 1, VEC>(a, P, s)          \
+     : a.E <= 128 ? RUN<T, 16, 1, VEC>(a, P, s)         \
+     : a.E <= 256 ? RUN<T, 32, 1, VEC>(a, P, s)         \
+     : a.E <= 512 ? RUN<T, 32, 2, VEC>(a, P, s)         \
+                  : RUN<T, 32, 4, VEC>(a, P, s))
+#define ROUTER_RUN(RUN, T) (vec ? ROUTER_BY_E(RUN, T, true) : ROUTER_BY_E(RUN, T, false))
 
 bool vectors(const void* p, int64_t ld, int E, int es, int64_t T) {
     return E % 8 == 0 && (uintptr_t)p % 16 == 0 && (T <= 1 || ld * es % 16 == 0);
@@ -816,10 +823,11 @@ cudaError_t launch_router_fwd(const void* logits, int64_t ld, const unsigned cha
     int* part_c = (int*)(part_p + P * E);
     if (P > 0) {
         const FwdArgs a{logits, mask, gates, ids, part_p, part_c, counts, loss, ld, (int)T, (int)E,
-                        (int)k, renorm, vectors(logits, ld, (int)E, elt_bytes(dtype), T)};
-        const cudaError_t e = dtype == 0   ? ROUTER_BY_E(run_fwd, float)
-                              : dtype == 1 ? ROUTER_BY_E(run_fwd, __half)
-                                           : ROUTER_BY_E(run_fwd, __nv_bfloat16);
+                        (int)k, renorm};
+        const bool vec = vectors(logits, ld, (int)E, elt_bytes(dtype), T);
+        const cudaError_t e = dtype == 0   ? ROUTER_RUN(run_fwd, float)
+                              : dtype == 1 ? ROUTER_RUN(run_fwd, __half)
+                                           : ROUTER_RUN(run_fwd, __nv_bfloat16);
         if (e != cudaSuccess || P == 1) return e;
     }
     const unsigned cs = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : 8;
@@ -834,11 +842,12 @@ cudaError_t launch_router_bwd(const void* logits, int64_t ld, const int* ids, co
     if (T == 0) return cudaSuccess;
     const int64_t P = blocks_for(T, E, true);
     const int es = elt_bytes(dtype);
-    const BwdArgs a{logits, ids, counts, dgates, dloss, dlogits, ld, ldd, (int)T, (int)E, (int)k, renorm,
-                    vectors(logits, ld, (int)E, es, T) && vectors(dlogits, ldd, (int)E, es, T)};
-    return dtype == 0   ? ROUTER_BY_E(run_bwd, float)
-           : dtype == 1 ? ROUTER_BY_E(run_bwd, __half)
-                        : ROUTER_BY_E(run_bwd, __nv_bfloat16);
+    const BwdArgs a{logits, ids, counts, dgates, dloss, dlogits, ld, ldd, (int)T, (int)E, (int)k,
+                    renorm};
+    const bool vec = vectors(logits, ld, (int)E, es, T) && vectors(dlogits, ldd, (int)E, es, T);
+    return dtype == 0   ? ROUTER_RUN(run_bwd, float)
+           : dtype == 1 ? ROUTER_RUN(run_bwd, __half)
+                        : ROUTER_RUN(run_bwd, __nv_bfloat16);
 }
 
 }  // namespace wsf
