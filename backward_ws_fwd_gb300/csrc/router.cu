@@ -268,6 +268,24 @@ struct Pick<float> {
     }
 };
 
+// Picks in shared memory by 32-bit addresses.
+template <typename P>
+__device__ __forceinline__ P get_pick(uint32_t a) {
+    P p;
+    if constexpr (sizeof(P) == 4)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(p.key) : "r"(a));
+    else
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(p.key), "=r"(p.low) : "r"(a));
+    return p;
+}
+template <typename P>
+__device__ __forceinline__ void put_pick(uint32_t a, const P& p) {
+    if constexpr (sizeof(P) == 4)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(p.key) : "memory");
+    else
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(p.key), "r"(p.low) : "memory");
+}
+
 // Sort eight descending: Batcher's odd-even merge sort, 19 comparators.
 template <typename P>
 __device__ __forceinline__ void sort8(P* a) {
@@ -324,6 +342,9 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
     const int E = a.E, k = a.k, T_ = a.T;
     P* run = runs + wid * 32 * 9 * R + lane;  // place q of run r: run[(r·9 + q)·32]
     P* mine = took + (wid * RPW + grp) * k;
+    constexpr uint32_t SP = sizeof(P);
+    const uint32_t at0 = (uint32_t)__cvta_generic_to_shared(run);
+    const uint32_t mine0 = (uint32_t)__cvta_generic_to_shared(mine);
 
     for (int i = threadIdx.x; i < SLOTS; i += NT) cnt[i] = 0;
 #pragma unroll
@@ -368,28 +389,30 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
             sort8(s);
             head[r] = Vec && x.past(r * 8, sub, E) ? P::of(0u, -1) : s[0];
 #pragma unroll
-            for (int q = 1; q < 8; q++) run[(r * 9 + q) * 32] = s[q];
+            for (int q = 1; q < 8; q++) put_pick(at0 + (r * 9 + q) * 32 * SP, s[q]);
         }
-        int at[R];  // the heads' places
+        uint32_t at[R], to = mine0;  // the heads' places; where the next choice goes
 #pragma unroll
-        for (int r = 0; r < R; r++) at[r] = r * 9 * 32;
-        P top = head[0];
+        for (int r = 0; r < R; r++) at[r] = at0 + r * 9 * 32 * SP;
+#pragma unroll 2
         for (int j = 0; j < k; j++) {
             P b = head[0];
 #pragma unroll
             for (int r = 1; r < R; r++)
                 if (head[r].above(b)) b = head[r];
             b = b.template best<L>();
-            if (j == 0) top = b;
-            if (sub == 0) mine[j] = b;
+            if (sub == 0) put_pick(to, b);
+            to += SP;
 #pragma unroll
             for (int r = 0; r < R; r++) {
-                const bool won = head[r].same(b);
-                at[r] += won ? 32 : 0;
-                if (won) head[r] = run[at[r]];
+                if (head[r].same(b)) {
+                    at[r] += 32 * SP;
+                    head[r] = get_pick<P>(at[r]);
+                }
             }
         }
-        float m = key_value<T>(top.key);
+        __syncwarp();
+        float m = key_value<T>(get_pick<P>(mine0).key);
         valid = valid && m != ninf();  // no logit above −inf: the row does not count
 
         // softmax, shifted by the largest
@@ -416,7 +439,6 @@ __global__ void __launch_bounds__(NT, R == 1 ? 4 : R == 2 ? 2 : 1)
         }
 
         // gates and ids
-        __syncwarp();
         if (a.renorm) {
             z = 0.f;
             for (int j = sub; j < k; j += L) z += exp_of(key_value<T>(mine[j].key), m);
