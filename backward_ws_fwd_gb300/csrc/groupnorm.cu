@@ -568,13 +568,14 @@ __global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T*
 
 // ---------------------------------------------------------------------------
 // Backward, first pass: a block walks units u0 .. u1 and writes each unit's
-// groups' sums (shares of M·m₂ and M·m₁) and, over all of them, the channels'.
+// groups' sums (shares of M·m₂ and M·m₁) and, over all of them, the channels',
+// which are added to the block's row of an earlier chunk (later).
 template <typename T, int V, bool Silu>
 __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, const T* dy, const float* w,
                                                          const float* b, const float* mean,
                                                          const float* rstd, const Shape d,
                                                          float* part_1, float* part_2, float* part_a,
-                                                         float* part_b) {
+                                                         float* part_b, const int later) {
     extern __shared__ float4 smem[];
     const Lanes t(d.C, V);
     // [RL][C], behind the staging
@@ -637,8 +638,8 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, c
         for (int c = threadIdx.x; c < d.C; c += NT) {
             float A = sa[c], B = sb[c];
             for (int r = 1; r < left; r++) A += sa[r * d.C + c], B += sb[r * d.C + c];
-            ta[c] = u > u0 ? ta[c] + A : A;
-            tb[c] = u > u0 ? tb[c] + B : B;
+            ta[c] = u > u0 || later ? ta[c] + A : A;
+            tb[c] = u > u0 || later ? tb[c] + B : B;
             sa[c] = A * __ldg(w + c);
             sb[c] = B * __ldg(w + c);
         }
@@ -660,14 +661,76 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, c
     }
 }
 
-// dx = dz·(w·r) − (x − μ)·(r²·m₂) − r·m₁
+// grad[c] (+)= Σ_p part[p, c] for both gradients, by a block of 32 columns: 8
+// stripes of rows (p ≡ stripe mod 8, in order), joined by a fixed tree, in
+// compensated pairs.
+struct Grads {
+    const float *part_a, *part_b;
+    float *gw, *gb;
+    int64_t P;
+    int C, accumulate;
+};
+
+__device__ __forceinline__ void grad_block(const Grads& d, int block, float4* smem) {
+    constexpr int W = NT / 32;
+    float2(*st)[33] = reinterpret_cast<float2(*)[33]>(smem);
+    const int col = threadIdx.x & 31, stripe = threadIdx.x >> 5;
+    const int c = block * 32 + col;
+    for (int which = 0; which < 2; which++) {
+        const float* part = which ? d.part_b : d.part_a;
+        Acc2 a = acc2_zero();
+        if (c < d.C) {
+            for (int64_t p = stripe; p < d.P; p += W * 8) {
+                float v[8];  // eight loads in flight
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    v[i] = p + W * i < d.P ? part[(p + W * i) * d.C + c] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) acc2_add1(a, v[i]);
+            }
+        }
+        st[stripe][col] = make_float2(a.hi, a.lo);
+        __syncthreads();
+        for (int h = W / 2; h > 0; h >>= 1) {
+            if (stripe < h) {
+                const float2 o = st[stripe + h][col];
+                a = acc2_add(a, Acc2{o.x, o.y});
+                st[stripe][col] = make_float2(a.hi, a.lo);
+            }
+            __syncthreads();
+        }
+        if (stripe == 0 && c < d.C) {
+            float* out = which ? d.gb : d.gw;
+            const float v = acc2_value(a);
+            out[c] = d.accumulate ? out[c] + v : v;
+        }
+    }
+}
+constexpr size_t kGradSmem = (NT / 32) * 33 * 8;
+
+__global__ void __launch_bounds__(NT) gn_grad_kernel(const Grads g) {
+    __shared__ float4 smem[kGradSmem / 16 + 1];
+    pdl_wait();
+    grad_block(g, blockIdx.x, smem);
+    pdl_trigger();
+}
+
+// Second pass: dx = dz·(w·r) − (x − μ)·(r²·m₂) − r·m₁.  The last chunk's first
+// `extra` blocks sum the parameter gradients beside it.
 template <typename T, int V, bool Silu>
 __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_apply_kernel(const T* x, const T* dy, T* dx,
                                                           const float* w, const float* b,
                                                           const float* mean, const float* rstd,
                                                           const float* part_1, const float* part_2,
-                                                          const Shape d) {
+                                                          const Shape d, const int extra,
+                                                          const Grads grads) {
     extern __shared__ float4 smem[];
+    if ((int)blockIdx.x < extra) {
+        pdl_wait();
+        grad_block(grads, blockIdx.x, smem);
+        pdl_trigger();
+        return;
+    }
     Walk<T, V, 2, kBwdStages> in;
     float4* st = smem + in.bytes / 16;  // [G] μ, r, −r·m₁, −r²·m₂
     const Lanes t(d.C, V);
@@ -725,45 +788,6 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_apply_kernel(const T* x, 
                 o += d.ystep;
             });
         }
-    }
-    pdl_trigger();
-}
-
-// grad[c] (+)= Σ_p part[p, c] for both gradients: 32 columns by 32 stripes of
-// rows (p ≡ stripe mod 32, in order), stripes joined by a fixed tree, in
-// compensated pairs.
-__global__ void __launch_bounds__(1024) gn_grad_kernel(const float* part_a, const float* part_b,
-                                                       int64_t P, int C, float* gw, float* gb,
-                                                       int accumulate) {
-    __shared__ float2 st[32][33];
-    pdl_wait();
-    const int col = threadIdx.x & 31, stripe = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + col;
-    const float* part = blockIdx.y ? part_b : part_a;
-    float* out = blockIdx.y ? gb : gw;
-    Acc2 a = acc2_zero();
-    if (c < C) {
-        for (int64_t p = stripe; p < P; p += 32 * 8) {
-            float v[8];  // eight loads in flight
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = p + 32 * i < P ? part[(p + 32 * i) * C + c] : 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; i++) acc2_add1(a, v[i]);
-        }
-    }
-    st[stripe][col] = make_float2(a.hi, a.lo);
-    __syncthreads();
-    for (int h = 16; h > 0; h >>= 1) {
-        if (stripe < h) {
-            const float2 o = st[stripe + h][col];
-            a = acc2_add(a, Acc2{o.x, o.y});
-            st[stripe][col] = make_float2(a.hi, a.lo);
-        }
-        __syncthreads();
-    }
-    if (stripe == 0 && c < C) {
-        const float v = acc2_value(a);
-        out[c] = accumulate ? out[c] + v : v;
     }
     pdl_trigger();
 }
@@ -1110,9 +1134,8 @@ cudaError_t rows_bwd(const GroupNormBwd& a, const RowShape& d, bool silu, cudaSt
         e = launch(k, dim3((unsigned)(d.segs * d.RB)), dim3(RT), smem, s, true, (const T*)a.x,
                    (const T*)a.dy, (T*)a.dx, a.w, a.b, a.mean, a.rstd, pa, pb, d);
     if (e != cudaSuccess) return e;
-    return launch(gn_grad_kernel, dim3((unsigned)((d.C + 31) / 32), 2), dim3(1024), 0, s, true,
-                  (const float*)pa, (const float*)pb, (int64_t)d.RB, d.C, a.grad_w, a.grad_b,
-                  a.accumulate);
+    return launch(gn_grad_kernel, dim3((unsigned)((d.C + 31) / 32)), dim3(NT), 0, s, true,
+                  Grads{pa, pb, a.grad_w, a.grad_b, d.RB, d.C, a.accumulate});
 }
 
 dim3 join_grid(const Shape& d) { return dim3((unsigned)((d.N * d.G + NT / 32 - 1) / (NT / 32))); }
@@ -1162,26 +1185,28 @@ cudaError_t fwd(const GroupNormFwd& a, Shape d, int64_t chunk, bool silu, cudaSt
 
 template <typename T, int V>
 cudaError_t bwd(const GroupNormBwd& a, Shape d, int64_t chunk, bool silu, cudaStream_t s) {
-    const int64_t P = grad_rows(d), chunks = a.N ? (a.N + chunk - 1) / chunk : 0;
+    const int64_t P = grad_rows(d);  // the first chunk is the largest
     float* pa = (float*)a.workspace;
-    float* pb = pa + pad64(chunks * P * d.C);
-    float* part_1 = pb + pad64(chunks * P * d.C);
+    float* pb = pa + pad64(P * d.C);
+    float* part_1 = pb + pad64(P * d.C);
     float* part_2 = part_1 + part_floats(d, chunk);
     constexpr size_t stage = Walk<T, V, 2, kBwdStages>::bytes;
-    const size_t smem = stage + 2 * lanes_bytes(d.C, V), smem2 = stage + (size_t)d.G * 16;
+    const size_t smem = stage + 2 * lanes_bytes(d.C, V);
+    const size_t smem2 = std::max(stage + (size_t)d.G * 16, kGradSmem);
     const auto sums = silu ? gn_bwd_sums_kernel<T, V, true> : gn_bwd_sums_kernel<T, V, false>;
     const auto apply = silu ? gn_bwd_apply_kernel<T, V, true> : gn_bwd_apply_kernel<T, V, false>;
     cudaError_t e = allow(sums, smem);
     if (e == cudaSuccess) e = allow(apply, smem2);
     steps(d, V);
-    int64_t rows = 0;
+    const int extra = (d.C + 31) / 32;
+    Shape d2 = d;
+    tile(d2, chunk, std::max(kDesignSMs, kDesignSMs * kBwdCtas - extra), (int)sizeof(T));
     for (int64_t n = 0; n < a.N && e == cudaSuccess; n += chunk) {
-        d.N = std::min(chunk, a.N - n);
-        const int64_t p = grad_rows(d);
+        d.N = d2.N = std::min(chunk, a.N - n);
         const T *x = (const T*)a.x + n * d.xn, *dy = (const T*)a.dy + n * d.gn;
         const float *mean = a.mean + n * d.G, *rstd = a.rstd + n * d.G;
-        e = launch(sums, dim3((unsigned)p), dim3(NT), smem, s, true, x, dy, a.w, a.b, mean, rstd, d,
-                   part_1, part_2, pa + rows * d.C, pb + rows * d.C);
+        e = launch(sums, dim3((unsigned)grad_rows(d)), dim3(NT), smem, s, true, x, dy, a.w, a.b,
+                   mean, rstd, d, part_1, part_2, pa, pb, (int)(n > 0));
         float *p1 = part_1, *p2 = part_2;
         if (e == cudaSuccess && d.joins < d.tiles) {
             float *j1 = p1 + chunk * d.tiles * d.G, *j2 = p2 + chunk * d.tiles * d.G;
@@ -1189,15 +1214,14 @@ cudaError_t bwd(const GroupNormBwd& a, Shape d, int64_t chunk, bool silu, cudaSt
                        (const float*)p2, j1, j2, d);
             p1 = j1, p2 = j2;
         }
+        const int more = n + chunk >= a.N ? extra : 0;
         if (e == cudaSuccess)
-            e = launch(apply, dim3((unsigned)(d.N * d.tiles)), dim3(NT), smem2, s, true, x, dy,
-                       (T*)a.dx + n * d.yn, a.w, a.b, mean, rstd, (const float*)p1,
-                       (const float*)p2, d);
-        rows += p;
+            e = launch(apply, dim3((unsigned)(d2.N * d2.tiles + more)), dim3(NT), smem2, s, true, x,
+                       dy, (T*)a.dx + n * d.yn, a.w, a.b, mean, rstd, (const float*)p1,
+                       (const float*)p2, d2, more,
+                       Grads{pa, pb, a.grad_w, a.grad_b, P, d.C, a.accumulate});
     }
-    if (e != cudaSuccess) return e;
-    return launch(gn_grad_kernel, dim3((unsigned)((d.C + 31) / 32), 2), dim3(1024), 0, s, true,
-                  (const float*)pa, (const float*)pb, rows, d.C, a.grad_w, a.grad_b, a.accumulate);
+    return e;
 }
 
 }  // namespace
@@ -1214,8 +1238,7 @@ int64_t groupnorm_bwd_floats(int64_t N, int64_t S, int64_t C, int64_t G, int dty
     if (N == 0 || S == 0 || C == 0) return 0;
     int64_t chunk;
     const Shape d = shape_of(N, S, C, G, elt_bytes(dtype), true, chunk);
-    const int64_t chunks = (N + chunk - 1) / chunk;
-    int64_t n = 2 * pad64(chunks * grad_rows(d) * C) + 2 * part_floats(d, chunk);
+    int64_t n = 2 * pad64(grad_rows(d) * C) + 2 * part_floats(d, chunk);
     RowShape r;  // taken or not by the pointers' alignment
     if (row_shape(N, S, C, G, elt_bytes(dtype), true, r)) n = std::max(n, 2 * pad64((int64_t)r.RB * C));
     return n;
@@ -1250,9 +1273,8 @@ cudaError_t launch_groupnorm_fwd(const GroupNormFwd& a, cudaStream_t s) {
 cudaError_t launch_groupnorm_bwd(const GroupNormBwd& a, cudaStream_t s) {
     const int es = elt_bytes(a.dtype);
     if (a.N == 0 || a.S == 0)  // no values: the gradients' sums are empty
-        return launch(gn_grad_kernel, dim3((unsigned)((a.C + 31) / 32), 2), dim3(1024), 0, s, true,
-                      (const float*)nullptr, (const float*)nullptr, (int64_t)0, (int)a.C, a.grad_w,
-                      a.grad_b, a.accumulate);
+        return launch(gn_grad_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(NT), 0, s, true,
+                      Grads{nullptr, nullptr, a.grad_w, a.grad_b, 0, (int)a.C, a.accumulate});
     int64_t k;
     Shape d = shape_of(a.N, a.S, a.C, a.G, es, true, k);
     d.xn = a.x_n, d.xs = a.x_s, d.yn = a.dx_n, d.ys = a.dx_s, d.gn = a.dy_n, d.gs = a.dy_s;

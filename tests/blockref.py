@@ -124,7 +124,8 @@ def groupnorm(x, w, b, G, eps, silu, dy=None):
     """dict of y, mean, rstd, dx, grad_w, grad_b and bounds *_tol.
 
     K = 128·U bounds the relative error of everything that leads to a
-    normalised value: at most 64 values a thread about a shift (64·U), joined
+    normalised value: at most 64 values a thread about a shift (64·U; tests of
+    longer samples keep to tiles of 64 rows a thread), joined
     over threads and tiles by trees (20·U), the square root, the division and
     the products of a value (10·U), and the 16-bit path's exponential and
     reciprocal (2^-21 = 8·U, and 2·|z|·U)."""

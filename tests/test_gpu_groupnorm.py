@@ -117,6 +117,16 @@ def test_offsets_outliers_and_constants(wsf, dtype, N, S, C, G):
     _check(wsf, flat.to(dtype), w, b, dy.to(dtype), G, "silu")
 
 
+def test_several_chunks(wsf):
+    """More values than the passes take at a time: uneven chunks of the batch
+    in both directions, gradients summed over them."""
+    x, w, b, dy = _inputs(9, 100000, 64, torch.float16, 17)
+    a = _check(wsf, x, w, b, dy, 4, "silu")
+    aw, ab = torch.full_like(a[4], 5.0), torch.full_like(a[5], 6.0)
+    wsf.groupnorm_bwd(x, w, b, a[1], a[2], dy, 4, "silu", grad_w=aw, grad_b=ab, accumulate=True)
+    assert torch.equal(aw, a[4] + 5.0) and torch.equal(ab, a[5] + 6.0)
+
+
 def test_samples_whose_passes_are_tiled_differently(wsf):
     """Numbers of samples for which the second pass cuts a sample into more
     tiles than the first."""
