@@ -51,7 +51,7 @@ SHAPES = [  # N, S, C, G
     (1, 1, 1, 1), (3, 1, 64, 8), (5, 1, 4096, 32), (700, 1, 512, 4), (37, 1, 2048, 8), (9, 1, 320, 5),
     (2, 1, 16384, 64), (64, 1, 96, 12), (1, 2, 2, 2), (2, 9, 30, 5), (3, 49, 320, 32), (2, 1024, 320, 32),
     (1, 4096, 128, 32), (4, 100, 200, 1), (2, 333, 64, 64), (1, 7, 8200, 8), (6, 17, 24, 3), (1, 5000, 40, 4),
-    (2, 257, 1280, 32), (1, 3, 16384, 1), (13, 64, 48, 16)]
+    (2, 257, 1280, 32), (1, 3, 16384, 1), (13, 64, 48, 16), (1, 4000, 512, 128)]
 
 
 @pytest.mark.parametrize("dtype", DTS)
