@@ -207,30 +207,27 @@ struct Walk {
         }
     }
 };
-// body(vectors, step) for every step of a walk.  Whole: full turns of the ring
-// run without a condition between the steps, so that one step's arithmetic
-// fills another's latencies, where the registers for it are there.
-template <bool Whole, typename T, int V, int K, int S, typename F>
+
+// body(vectors, step) for every step of a walk.  Full turns of the ring run
+// without a condition between the steps, so that one step's arithmetic fills
+// another's latencies.
+template <typename T, int V, int K, int S, typename F>
 __device__ __forceinline__ void each(Walk<T, V, K, S>& in, int count, F body) {
     int j = 0;
-    if constexpr (Whole) {
-        for (; j + S <= count; j += S) {
-#pragma unroll
-            for (int i = 0; i < S; i++) {
-                Held<T, V> h[K];
-                in.next(i, h);
-                body(h, j + i);
-            }
-        }
-    }
-    for (; j < count; j += S) {
+    for (; j + S <= count; j += S) {
 #pragma unroll
         for (int i = 0; i < S; i++) {
-            if (j + i < count) {
-                Held<T, V> h[K];
-                in.next(i, h);
-                body(h, j + i);
-            }
+            Held<T, V> h[K];
+            in.next(i, h);
+            body(h, j + i);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < S; i++) {
+        if (j + i < count) {
+            Held<T, V> h[K];
+            in.next(i, h);
+            body(h, j + i);
         }
     }
 }
@@ -367,6 +364,9 @@ __device__ __forceinline__ Vals<V> params(const float* p, int ch) {
 }
 
 // ---------------------------------------------------------------------------
+// (What the kernel before has written is read by __ldcg, from L2: this kernel
+// may have started before that one's last writes.)
+//
 // Any S: two passes over x, the second of which finds it in L2 (the host
 // takes the samples in chunks that fit; the second pass walks the tiles
 // backwards, so that of a sample that does not fit the end is still there).
@@ -376,8 +376,8 @@ __device__ __forceinline__ Vals<V> params(const float* p, int ch) {
 // about their common mean, first the row lanes of a channel (Q threads a
 // channel where there are few), then a group's channels by lg lanes.
 template <typename T, int V>
-__global__ void __launch_bounds__(NT, kStatsCtas) gn_stats_kernel(const T* x, const Shape d, float* part_m,
-                                                               float* part_q) {
+__global__ void __launch_bounds__(NT, kStatsCtas)
+    gn_stats_kernel(const T* x, const Shape d, float* part_m, float* part_q) {
     constexpr int S = kFwdStages;
     extern __shared__ float4 smem[];
     __shared__ float part_rows[NT];              // rows of a part
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(NT, kStatsCtas) gn_stats_kernel(const T* x, co
                 k = first.widen();
             }
             in.start(smem, cnt);
-            each<true>(in, cnt, [&](const Held<T, V>(&h)[1], int) {
+            each(in, cnt, [&](const Held<T, V>(&h)[1], int) {
                 const Vals<V> q = sub(h[0].widen(), k);
                 a = add(a, q);
                 b = fma(q, q, b);
@@ -491,16 +491,17 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(const float* pm, const floa
         float s = 0.f, q = 0.f;
 #pragma unroll 8
         for (int i = lane; i < d.tiles; i += 32) {
-            s = fmaf(Sums ? 1.f : i + 1 < d.tiles ? whole : last, pm[(int64_t)i * d.G], s);
-            if (Sums) q += pq[(int64_t)i * d.G];
+            s = fmaf(Sums ? 1.f : i + 1 < d.tiles ? whole : last, __ldcg(pm + (int64_t)i * d.G), s);
+            if (Sums) q += __ldcg(pq + (int64_t)i * d.G);
         }
         s = group_sum<32>(s);
         if (!Sums) {
             s /= (float)d.S;
 #pragma unroll 8
             for (int i = lane; i < d.tiles; i += 32) {
-                const float e = pm[(int64_t)i * d.G] - s;
-                q += fmaf((i + 1 < d.tiles ? whole : last) * d.Cg * e, e, pq[(int64_t)i * d.G]);
+                const float e = __ldcg(pm + (int64_t)i * d.G) - s;
+                q += fmaf((i + 1 < d.tiles ? whole : last) * d.Cg * e, e,
+                          __ldcg(pq + (int64_t)i * d.G));
             }
         }
         q = group_sum<32>(q);
@@ -509,15 +510,52 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(const float* pm, const floa
     pdl_trigger();
 }
 
-// Second pass.  The block first joins its sample's partial statistics, lg
-// lanes a group; the first tile's block writes the statistics out.  (Samples
+// Σ_i term(i, g) over a sample's partials, handed to done(g, sum) by one thread
+// a group: neighbouring threads take neighbouring groups, then neighbouring
+// partials, so that a warp reads whole lines, and the partials' sums meet in
+// shared memory (red, [NT]) in a fixed order.
+template <typename F, typename D>
+__device__ __forceinline__ void join(const Shape& d, float2* red, F term, D done) {
+    for (int g0 = 0; g0 < d.G; g0 += NT) {
+        const int G = min(d.G - g0, NT), parts = NT / G;
+        const int part = (int)threadIdx.x / G, g = g0 + (int)threadIdx.x - part * G;
+        float2 s = make_float2(0.f, 0.f);
+        if (part < parts) {
+            constexpr int U = 8;  // loads in flight
+            for (int i = part; i < d.joins; i += U * parts) {
+                float2 v[U];
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    v[u] = i + u * parts < d.joins ? term(i + u * parts, g) : make_float2(0.f, 0.f);
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    s.x += v[u].x;
+                    s.y += v[u].y;
+                }
+            }
+        }
+        red[threadIdx.x] = s;
+        __syncthreads();
+        if ((int)threadIdx.x < G) {
+            for (int q = 1; q < parts; q++) {
+                const float2 v = red[q * G + threadIdx.x];
+                s.x += v.x;
+                s.y += v.y;
+            }
+            done(g, s);
+        }
+        __syncthreads();
+    }
+}
+
+// Second pass.  The block first joins its sample's partial statistics; the
+// first tile's block writes them out.  (Samples
 // that are one tile in both passes keep their partial statistics where the
 // results go: the one block that reads them replaces them.)
 template <typename T, int V, bool Silu>
-__global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T* y, const float* w,
-                                                      const float* b, float eps, float* mean,
-                                                      float* rstd, const float* part_m,
-                                                      const float* part_q, const Shape d) {
+__global__ void __launch_bounds__(NT, kApplyCtas)
+    gn_apply_kernel(const T* x, T* y, const float* w, const float* b, float eps, float* mean,
+                    float* rstd, const float* part_m, const float* part_q, const Shape d) {
     extern __shared__ float4 smem[];
     Walk<T, V, 1, kFwdStages> in;
     float2* st = reinterpret_cast<float2*>(smem) + in.bytes / 8;  // [G] μ, r
@@ -533,36 +571,33 @@ __global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T*
     };
     pdl_wait();
     begin(t.c);  // in flight while the tiles are joined
-    const int j0 = threadIdx.x & (d.lg - 1);
-    for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
-        const int g = g0 + threadIdx.x / d.lg;
-        const bool on = g < d.G;
-        const float* pm = part_m + (int64_t)un.n * d.joins * d.G + g;
-        const float* pq = part_q + (int64_t)un.n * d.joins * d.G + g;
-        const float whole = (float)d.jrows, last = (float)(d.S - (d.joins - 1) * d.jrows);
-        float s = 0.f;
-        if (on) {
-#pragma unroll 4
-            for (int i = j0; i < d.joins; i += d.lg)
-                s = fmaf(i + 1 < d.joins ? whole : last, pm[(int64_t)i * d.G], s);
-        }
-        const float m = lanes_sum(s, d.lg) / (float)d.S;
-        s = 0.f;
-        if (on) {
-#pragma unroll 4
-            for (int i = j0; i < d.joins; i += d.lg) {
-                const float e = pm[(int64_t)i * d.G] - m;
-                s += fmaf((i + 1 < d.joins ? whole : last) * d.Cg * e, e, pq[(int64_t)i * d.G]);
+    __shared__ float2 red[NT];
+    const float* pm = part_m + (int64_t)un.n * d.joins * d.G;
+    const float* pq = part_q + (int64_t)un.n * d.joins * d.G;
+    const float whole = (float)d.jrows, last = (float)(d.S - (d.joins - 1) * d.jrows);
+    const float all = (float)d.S;
+    join(
+        d, red,
+        [&](int i, int g) {
+            return make_float2((i + 1 < d.joins ? whole : last) * __ldcg(pm + (int64_t)i * d.G + g),
+                               0.f);
+        },
+        [&](int g, float2 s) { st[g].x = s.x / all; });
+    join(
+        d, red,
+        [&](int i, int g) {
+            const float e = __ldcg(pm + (int64_t)i * d.G + g) - st[g].x;
+            const float n = (i + 1 < d.joins ? whole : last) * d.Cg;
+            return make_float2(fmaf(n * e, e, __ldcg(pq + (int64_t)i * d.G + g)), 0.f);
+        },
+        [&](int g, float2 s) {
+            const float r = 1.0f / sqrtf(s.x / (all * d.Cg) + eps);
+            st[g].y = r;
+            if (un.tile == 0) {
+                mean[(int64_t)un.n * d.G + g] = st[g].x;
+                rstd[(int64_t)un.n * d.G + g] = r;
             }
-        }
-        s = lanes_sum(s, d.lg);
-        if (on && j0 == 0) {
-            const float r = 1.0f / sqrtf(s / ((float)d.S * d.Cg) + eps);
-            st[g] = make_float2(m, r);
-            if (un.tile == 0) mean[(int64_t)un.n * d.G + g] = m, rstd[(int64_t)un.n * d.G + g] = r;
-        }
-    }
-    __syncthreads();
+        });
     if (t.r < t.RL) {
         for (int c = t.c; c < t.cv; c += NT) {
             if (c != t.c) begin(c);
@@ -571,7 +606,7 @@ __global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T*
                                    params<V>(w, c * V));
             const Vals<V> sh = params<V>(b, c * V);
             T* o = y + un.n * d.yn + (un.s0 + t.r) * d.ys + c * V;
-            each<true>(in, cnt, [&](const Held<T, V>(&h)[1], int) {
+            each(in, cnt, [&](const Held<T, V>(&h)[1], int) {
                 store_v<T, V>(o, activate<T, Silu, V>(fma(sub(h[0].widen(), mu), rw, sh)));
                 o += d.ystep;
             });
@@ -585,11 +620,10 @@ __global__ void __launch_bounds__(NT, kApplyCtas) gn_apply_kernel(const T* x, T*
 // groups' sums (shares of M·m₂ and M·m₁) and, over all of them, the channels',
 // which are added to the block's row of an earlier chunk (later).
 template <typename T, int V, bool Silu>
-__global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, const T* dy, const float* w,
-                                                         const float* b, const float* mean,
-                                                         const float* rstd, const Shape d,
-                                                         float* part_1, float* part_2, float* part_a,
-                                                         float* part_b, const int later) {
+__global__ void __launch_bounds__(NT, kBwdCtas)
+    gn_bwd_sums_kernel(const T* x, const T* dy, const float* w, const float* b, const float* mean,
+                       const float* rstd, const Shape d, float* part_1, float* part_2,
+                       float* part_a, float* part_b, const int later) {
     extern __shared__ float4 smem[];
     const Lanes t(d.C, V);
     // [RL][C], behind the staging
@@ -622,7 +656,7 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, c
                                        params<V>(w, c * V));
                 const Vals<V> bc = params<V>(b, c * V);
                 Vals<V> A = Vals<V>::splat(0.f), B = A;
-                each<true>(in, cnt, [&](const Held<T, V>(&h)[2], int) {
+                each(in, cnt, [&](const Held<T, V>(&h)[2], int) {
                     const Vals<V> f = sub(h[0].widen(), mu);
                     const Vals<V> dz = through<T, Silu, V>(h[1].widen(), fma(f, rw, bc));
                     A = fma(dz, f, A);  // times r below
@@ -652,8 +686,9 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_sums_kernel(const T* x, c
         for (int c = threadIdx.x; c < d.C; c += NT) {
             float A = sa[c], B = sb[c];
             for (int r = 1; r < left; r++) A += sa[r * d.C + c], B += sb[r * d.C + c];
-            ta[c] = u > u0 || later ? ta[c] + A : A;
-            tb[c] = u > u0 || later ? tb[c] + B : B;
+            const bool more = u > u0 || later;
+            ta[c] = more ? __ldcg(ta + c) + A : A;
+            tb[c] = more ? __ldcg(tb + c) + B : B;
             sa[c] = A * __ldg(w + c);
             sb[c] = B * __ldg(w + c);
         }
@@ -698,7 +733,7 @@ __device__ __forceinline__ void grad_block(const Grads& d, int block, float4* sm
                 float v[8];  // eight loads in flight
 #pragma unroll
                 for (int i = 0; i < 8; i++)
-                    v[i] = p + W * i < d.P ? part[(p + W * i) * d.C + c] : 0.f;
+                    v[i] = p + W * i < d.P ? __ldcg(part + (p + W * i) * d.C + c) : 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; i++) acc2_add1(a, v[i]);
             }
@@ -732,12 +767,10 @@ __global__ void __launch_bounds__(NT) gn_grad_kernel(const Grads g) {
 // Second pass: dx = dz·(w·r) − (x − μ)·(r²·m₂) − r·m₁.  The last chunk's first
 // `extra` blocks sum the parameter gradients beside it.
 template <typename T, int V, bool Silu>
-__global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_apply_kernel(const T* x, const T* dy, T* dx,
-                                                          const float* w, const float* b,
-                                                          const float* mean, const float* rstd,
-                                                          const float* part_1, const float* part_2,
-                                                          const Shape d, const int extra,
-                                                          const Grads grads) {
+__global__ void __launch_bounds__(NT, kBwdCtas)
+    gn_bwd_apply_kernel(const T* x, const T* dy, T* dx, const float* w, const float* b,
+                        const float* mean, const float* rstd, const float* part_1,
+                        const float* part_2, const Shape d, const int extra, const Grads grads) {
     extern __shared__ float4 smem[];
     if ((int)blockIdx.x < extra) {
         pdl_wait();
@@ -762,29 +795,20 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_apply_kernel(const T* x, 
     };
     pdl_wait();
     begin(t.c);  // in flight while the tiles are joined
-    const int j0 = threadIdx.x & (d.lg - 1);
+    __shared__ float2 red[NT];
     const float inv = 1.0f / ((float)d.S * d.Cg);
-    for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
-        const int g = g0 + threadIdx.x / d.lg;
-        const bool on = g < d.G;
-        const float* p1 = part_1 + (int64_t)un.n * d.joins * d.G + g;
-        const float* p2 = part_2 + (int64_t)un.n * d.joins * d.G + g;
-        float A = 0.f, B = 0.f;
-        if (on) {
-#pragma unroll 4
-            for (int i = j0; i < d.joins; i += d.lg) {
-                A += p2[(int64_t)i * d.G];
-                B += p1[(int64_t)i * d.G];
-            }
-        }
-        A = lanes_sum(A, d.lg);
-        B = lanes_sum(B, d.lg);
-        if (on && j0 == 0) {
+    const float* p1 = part_1 + (int64_t)un.n * d.joins * d.G;
+    const float* p2 = part_2 + (int64_t)un.n * d.joins * d.G;
+    join(
+        d, red,
+        [&](int i, int g) {
+            return make_float2(__ldcg(p1 + (int64_t)i * d.G + g), __ldcg(p2 + (int64_t)i * d.G + g));
+        },
+        [&](int g, float2 s) {
             const float r = rstd[(int64_t)un.n * d.G + g];
-            st[g] = make_float4(mean[(int64_t)un.n * d.G + g], r, -r * (B * inv), -r * r * (A * inv));
-        }
-    }
-    __syncthreads();
+            st[g] = make_float4(mean[(int64_t)un.n * d.G + g], r, -r * (s.x * inv),
+                                -r * r * (s.y * inv));
+        });
     if (t.r < t.RL) {
         for (int c = t.c; c < t.cv; c += NT) {
             if (c != t.c) begin(c);
@@ -795,7 +819,7 @@ __global__ void __launch_bounds__(NT, kBwdCtas) gn_bwd_apply_kernel(const T* x, 
             const Vals<V> e2 = by_group<V>(c * V, d.Cg, [&](int g) { return st[g].w; });
             const Vals<V> bc = params<V>(b, c * V);
             T* o = dx + un.n * d.yn + (un.s0 + t.r) * d.ys + c * V;
-            each<true>(in, cnt, [&](const Held<T, V>(&h)[2], int) {
+            each(in, cnt, [&](const Held<T, V>(&h)[2], int) {
                 const Vals<V> f = sub(h[0].widen(), mu);
                 const Vals<V> dz = through<T, Silu, V>(h[1].widen(), fma(f, rw, bc));
                 store_v<T, V>(o, fma(dz, rw, fma(f, e2, e1)));
@@ -872,7 +896,7 @@ __global__ void __launch_bounds__(RT, CPL == 1 ? kRowsFwdCtas : 2)
     in.policy = l2_evict_first();
     in.start(smem, mine);
     T* o = y + n * d.yn + t.at;
-    each<true>(in, turns, [&](Held<T, V>(&h)[CPL], int turn) {
+    each(in, turns, [&](Held<T, V>(&h)[CPL], int turn) {
         Vals<V> f[CPL], q = Vals<V>::splat(0.f);
 #pragma unroll
         for (int c = 0; c < CPL; c++) {
@@ -971,7 +995,7 @@ __global__ void __launch_bounds__(RT, CPL == 1 ? kRowsBwdCtas : 2)
     // the statistics, a turn ahead
     const float *mp = mean + (mine ? n : 0) * d.G + t.g, *rp = rstd + (mine ? n : 0) * d.G + t.g;
     float mu = __ldg(mp), rs = __ldg(rp);
-    each<true>(in, turns, [&](Held<T, V>(&h)[2 * CPL], int turn) {
+    each(in, turns, [&](Held<T, V>(&h)[2 * CPL], int turn) {
         const float m0 = mu, r0 = rs;
         if (turn + 1 < mine) {
             mp += d.step * d.G;

@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(RT) router_reduce_kernel(const float* part_p, 
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const bool in = e < E && p0 + 32 * i < P;
-                v[i] = in ? __ldg(part_p + (int64_t)(p0 + 32 * i) * E + e) : 0.f;
-                n[i] = in ? __ldg(part_c + (int64_t)(p0 + 32 * i) * E + e) : 0;
+                v[i] = in ? __ldcg(part_p + (int64_t)(p0 + 32 * i) * E + e) : 0.f;
+                n[i] = in ? __ldcg(part_c + (int64_t)(p0 + 32 * i) * E + e) : 0;
             }
 #pragma unroll
             for (int i = 0; i < 8; i++) acc2_add1(s, v[i]), c += n[i];
@@ -621,7 +621,7 @@ __device__ __forceinline__ void store_row(T* row, int sub, int E, const float (&
 
 template <int L, int R>
 size_t bwd_smem() {
-    return (size_t)NW * 32 * 8 * R * 4 + 64;
+    return (size_t)NW * 32 * 8 * R * 4 + NW * 8 + (size_t)L * 8 * R * 4;
 }
 
 template <typename T, int L, int R, bool Vec, bool Renorm>
@@ -636,9 +636,13 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
     const int E = a.E, k = a.k;
     float* mine = put + (wid * RPW + grp) * SLOTS;
     for (int i = threadIdx.x; i < NW * RPW * SLOTS; i += NT) put[i] = 0.f;
+    int* cnt = reinterpret_cast<int*>(tot + NW);  // [SLOTS]
     pdl_wait();
     long long ch = 0;
-    for (int e = threadIdx.x; e < E; e += NT) ch += a.counts[e];
+    for (int e = threadIdx.x; e < SLOTS; e += NT) {
+        cnt[e] = e < E ? __ldcg(a.counts + e) : 0;
+        ch += cnt[e];
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ch += __shfl_xor_sync(FULL_MASK, ch, o);
     if (lane == 0) tot[wid] = ch;
@@ -653,8 +657,7 @@ __global__ void __launch_bounds__(NT, R == 1 ? 3 : R == 2 ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < EPL; i += 2) {
         const int e = expert<L>(i, sub);
-        ae[i / 2] = f2_pack(e < E ? unit * (float)a.counts[e] : 0.f,
-                            e + 1 < E ? unit * (float)a.counts[e + 1] : 0.f);
+        ae[i / 2] = f2_pack(unit * (float)cnt[e], unit * (float)cnt[e + 1]);
     }
 
     const int step = gridDim.x * NW * RPW, T_ = a.T;

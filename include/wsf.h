@@ -24,7 +24,8 @@
  * library allocates nothing, keeps no state between calls, and never frees
  * caller memory.  A pointer may be NULL only when the buffer it addresses
  * has no elements.  Outputs must not overlap any input or each other
- * (checked on the host; WSF_ERR_OVERLAP).
+ * (checked on the host; WSF_ERR_OVERLAP), but for rotary_fwd / rotary_bwd in
+ * place.
  *
  * Types.  `dtype` is the storage type of x, dy, y and dx: WSF_F32, WSF_F16
  * (IEEE binary16) or WSF_BF16 (bfloat16).  w, grad_w and dw are always
@@ -321,7 +322,8 @@ int layernorm_bwd(const void* x, int64_t ldx, const float* w, const void* dy, in
  * stride along S, row stride ld_positions (0: one row for every batch).
  * inv_freq: [R/2] binary32, radians a token.  The angle is the exact product
  * position·inv_freq reduced modulo a turn, within 2e-7 rad for positions of up
- * to 2^40 (a frequency that is not finite gives NaN); products are binary32 and each output is rounded once.
+ * to 2^38 (a frequency that is not finite gives NaN); products are binary32
+ * and each output is rounded once.
  * In place: yq may be q itself (same address, same strides), and yk k;
  * otherwise outputs must not overlap inputs or one another.  Interleaved
  * views of one packed buffer that share their batch and token strides do not

@@ -222,18 +222,28 @@ def test_same_bits(wsf):
 
 
 def test_large_offsets(wsf):
-    """Samples whose elements lie behind the 2^31st of their tensor."""
-    N, S, C, G, step = 3, 4, 64, 4, 1 << 30
-    buf = torch.zeros((N - 1) * step + S * C, dtype=torch.bfloat16, device=DEV)
-    x = buf.as_strided((N, S, C), (step, C, 1))
-    x0, w, b, dy = _inputs(N, S, C, torch.bfloat16, 12)
-    x.copy_(x0)
-    y, mean, rstd = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu")
-    want = wsf.groupnorm_fwd(x0, w, b, G, EPS, "silu")
-    assert torch.equal(y, want[0]) and torch.equal(mean, want[1])
-    d = wsf.groupnorm_bwd(x, w, b, mean, rstd, dy, G, "silu")
-    for p, q in zip(d, wsf.groupnorm_bwd(x0, w, b, mean, rstd, dy, G, "silu")):
-        assert torch.equal(p, q)
+    """Samples, rows and heads whose elements lie behind the 2^31st of their
+    tensors, read and written."""
+    for N, S, C, G, sn, ss in ((3, 4, 64, 4, 1 << 30, 64), (2, 40000, 64, 4, 40000 * 32768, 32768),
+                               (70000, 1, 128, 2, 32768, 128)):
+        x0, w, b, dy = _inputs(N, S, C, torch.bfloat16, 12)
+        size = (N - 1) * sn + (S - 1) * ss + C
+        assert size > 1 << 31
+
+        def far(t=None):
+            v = torch.zeros(size, dtype=torch.bfloat16, device=DEV).as_strided((N, S, C), (sn, ss, 1))
+            return v if t is None else v.copy_(t)
+
+        x, y = far(x0), far()
+        _, mean, rstd = wsf.groupnorm_fwd(x, w, b, G, EPS, "silu", y=y)
+        want = wsf.groupnorm_fwd(x0, w, b, G, EPS, "silu")
+        assert torch.equal(y, want[0]) and torch.equal(mean, want[1])
+        del y
+        dx = far()
+        _, gw, gb = wsf.groupnorm_bwd(x, w, b, mean, rstd, dy, G, "silu", dx=dx)
+        for p, q in zip((dx, gw, gb), wsf.groupnorm_bwd(x0, w, b, mean, rstd, dy, G, "silu")):
+            assert torch.equal(p, q)
+        del x, dx
 
 
 def test_many_groups(wsf):

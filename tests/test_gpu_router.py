@@ -147,6 +147,25 @@ def test_strides_and_guards(wsf, dtype, E, pad, mis):
     assert bool((out[keep] == 7.0).all())
 
 
+def test_large_offsets(wsf):
+    """Rows whose elements lie behind the 2^31st, read and written."""
+    T, E, ld = 70000, 24, 32768
+    buf = torch.zeros((T - 1) * ld + E, dtype=torch.bfloat16, device=DEV)
+    l = buf.as_strided((T, E), (ld, 1))
+    src = _logits(T, E, torch.bfloat16, 15)
+    l.copy_(src)
+    assert (T - 1) * ld > 1 << 31
+    want = _check(wsf, src, 4)
+    got = wsf.router_fwd(l, 4)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    g = torch.Generator(device=DEV).manual_seed(0)
+    out = torch.zeros((T - 1) * ld + E, dtype=torch.bfloat16, device=DEV).as_strided((T, E), (ld, 1))
+    wsf.router_bwd(l, got[1], got[2], torch.randn(T, 4, generator=g, device=DEV), torch.tensor(0.7, device=DEV),
+                   dlogits=out)
+    assert torch.equal(out, want[4])
+
+
 def test_large_spread(wsf):
     """Logits hundreds apart: probabilities down to 0, no overflow."""
     for dtype in DTS:
