@@ -16,8 +16,8 @@
 // values in 32 groups: 147 us, 5550 GB/s of the 6780 of a copy); other samples
 // take two passes.  Of those the second finds in L2 what fits there (forward of
 // 32 x 64 x 64 x 320 bf16 values 44 us; read and written once they would take 25)
-// and reads the rest again (backward of 4 x 512 x 512 x 128 fp16 values 239 us, of
-// which reading x and dy twice and writing dx would take 198).
+// and reads the rest again (backward of 4 x 512 x 512 x 128 fp16 values 225 us;
+// reading x and dy twice and writing dx would take 198, once each 119).
 //
 // A thread keeps one 16-byte vector of channels and walks the rows of a
 // tile.  Statistics of a tile: sums of x and x² about the thread's first
@@ -36,10 +36,10 @@ namespace {
 
 constexpr int NT = 256;
 // Stages of Walk.  Forward of 32 x 64 x 64 x 320: 44 us with 8, 45 with 6, 48
-// with 4; backward of 4 x 512 x 512 x 128: 242 with 6, 244 with 4 and 8.
+// with 4; backward of 4 x 512 x 512 x 128: 226 with 6, 230 with 4 and 8.
 constexpr int kFwdStages = 8, kBwdStages = 6, kRowStages = 6;
 // Blocks that an SM holds at once, by kernel: few enough that the whole turns of
-// a walk keep their values in registers (backward: 242 us with two, 270 with
+// a walk keep their values in registers (backward: 226 us with two, 265 with
 // three; rows backward 148 with three, 157 with two, 167 with four).
 constexpr int kStatsCtas = 2, kApplyCtas = 3, kBwdCtas = 2, kRowsFwdCtas = 4, kRowsBwdCtas = 3;
 
@@ -474,8 +474,8 @@ __global__ void __launch_bounds__(NT, kStatsCtas)
 // Where a sample has many partial statistics (or sums), tiles x groups, they
 // are joined by a warp a (sample, group) before the second pass; fewer are
 // joined by every block of the second pass itself, which saves a launch
-// (304 tiles of 32 groups: backward of 4 x 512 x 512 x 128 values 239 us in
-// place of 241; 14 tiles: forward of 32 x 64 x 64 x 320 values 44 in place of 47).
+// (304 tiles of 32 groups: backward of 4 x 512 x 512 x 128 values 226 us in
+// place of 242; 14 tiles: forward of 32 x 64 x 64 x 320 values 44 in place of 47).
 constexpr int kJoin = 16384;
 
 template <bool Sums>
@@ -1061,7 +1061,7 @@ __global__ void __launch_bounds__(RT, CPL == 1 ? kRowsBwdCtas : 2)
 
 // Cut a sample into row tiles: as many as give the chunk at most `blocks`
 // blocks (a number that the SMs hold at once, so that none waits for a second
-// turn: backward of 4 x 512 x 512 x 128 242 us, with twice as many 295), of 16 KB
+// turn: backward of 4 x 512 x 512 x 128 226 us, with twice as many 282), of 16 KB
 // or more each.
 void tile(Shape& d, int64_t chunk, int64_t blocks, int es) {
     const int64_t most = std::max<int64_t>(1, blocks / chunk);
@@ -1072,10 +1072,9 @@ void tile(Shape& d, int64_t chunk, int64_t blocks, int es) {
 }
 
 // chunk: samples of one pair of passes, whose tensors (x, or x and dy) fit in
-// L2 (forward of 32 x 64 x 64 x 320, 84 MB: 44 us in one chunk, 57 in two, 81 in
-// three).  The tiles are the first pass's.  Of a sample that does not fit, the
-// first pass keeps the end, which the second pass reads first (64 MB; 96 MB
-// measured 2% slower).
+// L2 (forward of 32 x 64 x 64 x 320, 84 MB: 44 us in one chunk, 56 in two).  The tiles are the first pass's.  Of a sample that does not fit, the
+// first pass keeps the end, which the second pass reads first (backward of 4 x
+// 512 x 512 x 128: 226 us with 64 MB kept, 233 with 32, 227 with 96).
 constexpr int64_t kL2Chunk = 96 << 20, kL2Keep = 64 << 20;
 
 Shape shape_of(int64_t N, int64_t S, int64_t C, int64_t G, int es, bool backward, int64_t& chunk) {
