@@ -142,7 +142,7 @@ __device__ __forceinline__ void store_v(T* p, const Vals<V>& v) {
 // cp.async of 16 bytes under an L2 policy.
 __device__ __forceinline__ void cp_async16_hint(void* smem, const void* gmem, uint64_t policy) {
     const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2;" ::"r"(s),
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(s),
                  "l"(gmem), "l"(policy)
                  : "memory");
 }
@@ -364,8 +364,8 @@ __device__ __forceinline__ Vals<V> params(const float* p, int ch) {
 }
 
 // ---------------------------------------------------------------------------
-// (What the kernel before has written is read by __ldcg, from L2: this kernel
-// may have started before that one's last writes.)
+// (What the kernel before has written is not read by the read-only path: this
+// kernel may have started before that one's last writes.)
 //
 // Any S: two passes over x, the second of which finds it in L2 (the host
 // takes the samples in chunks that fit; the second pass walks the tiles
@@ -405,12 +405,13 @@ __global__ void __launch_bounds__(NT, kStatsCtas)
             in.step[0] = d.xstep;
             in.use[0] = true;
             in.policy = un.tile < d.keep ? l2_evict_first() : l2_evict_normal();
-            Held<T, V> first;
-            if (cnt) {
-                first.load(in.p[0]);
-                k = first.widen();
-            }
+            const T* first = in.p[0];
             in.start(smem, cnt);
+            if (cnt) {  // (once more, beside the ring)
+                Held<T, V> h;
+                h.load(first);
+                k = h.widen();
+            }
             each(in, cnt, [&](const Held<T, V>(&h)[1], int) {
                 const Vals<V> q = sub(h[0].widen(), k);
                 a = add(a, q);
@@ -521,7 +522,7 @@ __device__ __forceinline__ void join(const Shape& d, float2* red, F term, D done
         const int part = (int)threadIdx.x / G, g = g0 + (int)threadIdx.x - part * G;
         float2 s = make_float2(0.f, 0.f);
         if (part < parts) {
-            constexpr int U = 8;  // loads in flight
+            constexpr int U = 16;  // loads in flight
             for (int i = part; i < d.joins; i += U * parts) {
                 float2 v[U];
 #pragma unroll
@@ -579,16 +580,15 @@ __global__ void __launch_bounds__(NT, kApplyCtas)
     join(
         d, red,
         [&](int i, int g) {
-            return make_float2((i + 1 < d.joins ? whole : last) * __ldcg(pm + (int64_t)i * d.G + g),
-                               0.f);
+            return make_float2((i + 1 < d.joins ? whole : last) * pm[(int64_t)i * d.G + g], 0.f);
         },
         [&](int g, float2 s) { st[g].x = s.x / all; });
     join(
         d, red,
         [&](int i, int g) {
-            const float e = __ldcg(pm + (int64_t)i * d.G + g) - st[g].x;
+            const float e = pm[(int64_t)i * d.G + g] - st[g].x;  // (from L1 now)
             const float n = (i + 1 < d.joins ? whole : last) * d.Cg;
-            return make_float2(fmaf(n * e, e, __ldcg(pq + (int64_t)i * d.G + g)), 0.f);
+            return make_float2(fmaf(n * e, e, pq[(int64_t)i * d.G + g]), 0.f);
         },
         [&](int g, float2 s) {
             const float r = 1.0f / sqrtf(s.x / (all * d.Cg) + eps);
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(NT, kBwdCtas)
     join(
         d, red,
         [&](int i, int g) {
-            return make_float2(__ldcg(p1 + (int64_t)i * d.G + g), __ldcg(p2 + (int64_t)i * d.G + g));
+            return make_float2(p1[(int64_t)i * d.G + g], p2[(int64_t)i * d.G + g]);
         },
         [&](int g, float2 s) {
             const float r = rstd[(int64_t)un.n * d.G + g];
