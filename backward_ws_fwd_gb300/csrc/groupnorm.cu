@@ -16,8 +16,10 @@
 // values in 32 groups: 147 us, 5550 GB/s of the 6780 of a copy); other samples
 // take two passes.  Of those the second finds in L2 what fits there (forward of
 // 32 x 64 x 64 x 320 bf16 values 44 us; read and written once they would take 25)
-// and reads the rest again (backward of 4 x 512 x 512 x 128 fp16 values 225 us;
-// reading x and dy twice and writing dx would take 198, once each 119).
+// and reads the rest again (backward of 4 x 512 x 512 x 128 fp16 values 220 us;
+// reading x and dy twice and writing dx would take 198, once each 119).  The
+// figures at the constants below compare both sides of a choice at the time
+// that it was made.
 //
 // A thread keeps one 16-byte vector of channels and walks the rows of a
 // tile.  Statistics of a tile: sums of x and x² about the thread's first
