@@ -28,6 +28,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "wsf_block.h"
 #include "wsf_device.cuh"
@@ -1112,12 +1113,23 @@ size_t lanes_bytes(int C, int V) {
     return (size_t)(cv < NT ? NT / cv : 1) * C * 4;
 }
 
-template <typename K>
-cudaError_t allow(K kernel, size_t smem) {
-    return smem <= 40 * 1024 ? cudaSuccess
-                             : cudaFuncSetAttribute((const void*)kernel,
-                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    (int)smem);
+// Let a kernel take as much dynamic shared memory as any size here needs (C =
+// 16,384: 179 KB), once a device; kernels that stay below the default need not
+// ask (a call of it takes about a microsecond).
+constexpr int kMostSmem = 200 * 1024;
+
+template <auto kernel>
+cudaError_t allow(size_t smem) {
+    static std::atomic<bool> done[kMaxDevices];
+    if (smem <= 40 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMostSmem);
+    if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 // Whether S == 1 rows take the row kernels, and their shape: 16-byte vectors
@@ -1152,7 +1164,8 @@ template <typename T, int CPL>
 cudaError_t rows_fwd(const GroupNormFwd& a, const RowShape& d, bool silu, cudaStream_t s) {
     const auto k = silu ? gn_rows_fwd_kernel<T, CPL, true> : gn_rows_fwd_kernel<T, CPL, false>;
     constexpr size_t smem = Walk<T, Elt<T>::V, CPL, kFwdStages>::bytes;
-    const cudaError_t e = allow(k, smem);
+    const cudaError_t e = silu ? allow<gn_rows_fwd_kernel<T, CPL, true>>(smem)
+                               : allow<gn_rows_fwd_kernel<T, CPL, false>>(smem);
     if (e != cudaSuccess) return e;
     return launch(k, dim3((unsigned)(d.segs * d.RB)), dim3(RT), smem, s, true, (const T*)a.x,
                   (T*)a.y, a.w, a.b, a.eps, a.mean, a.rstd, d);
@@ -1166,7 +1179,8 @@ cudaError_t rows_bwd(const GroupNormBwd& a, const RowShape& d, bool silu, cudaSt
     constexpr size_t stage = Walk<T, Elt<T>::V, 2 * CPL, CPL == 1 ? kRowStages : kRowStages / 2>::bytes;
     constexpr size_t smem = std::max(stage, (size_t)2 * RW * CPL * Elt<T>::V * 32 * 4) +
                             (size_t)2 * CPL * Elt<T>::V * 32 * 4;
-    cudaError_t e = allow(k, smem);
+    cudaError_t e = silu ? allow<gn_rows_bwd_kernel<T, CPL, true>>(smem)
+                         : allow<gn_rows_bwd_kernel<T, CPL, false>>(smem);
     if (e == cudaSuccess)
         e = launch(k, dim3((unsigned)(d.segs * d.RB)), dim3(RT), smem, s, true, (const T*)a.x,
                    (const T*)a.dy, (T*)a.dx, a.w, a.b, a.mean, a.rstd, pa, pb, d);
@@ -1193,8 +1207,10 @@ cudaError_t fwd(const GroupNormFwd& a, Shape d, int64_t chunk, bool silu, cudaSt
     constexpr size_t stage = Walk<T, V, 1, kFwdStages>::bytes;
     const size_t smem = stage + 2 * lanes_bytes(d.C, V), smem2 = stage + (size_t)d.G * 8;
     const auto apply = silu ? gn_apply_kernel<T, V, true> : gn_apply_kernel<T, V, false>;
-    cudaError_t e = allow(gn_stats_kernel<T, V>, smem);
-    if (e == cudaSuccess) e = allow(apply, smem2);
+    cudaError_t e = allow<gn_stats_kernel<T, V>>(smem);
+    if (e == cudaSuccess)
+        e = silu ? allow<gn_apply_kernel<T, V, true>>(smem2)
+                 : allow<gn_apply_kernel<T, V, false>>(smem2);
     steps(d, V);
     const Shape t2 = second_tiles(d, chunk, (int)sizeof(T));
     const bool whole = d.tiles == 1 && t2.tiles == 1;
@@ -1232,8 +1248,11 @@ cudaError_t bwd(const GroupNormBwd& a, Shape d, int64_t chunk, bool silu, cudaSt
     const size_t smem2 = std::max(stage + (size_t)d.G * 16, kGradSmem);
     const auto sums = silu ? gn_bwd_sums_kernel<T, V, true> : gn_bwd_sums_kernel<T, V, false>;
     const auto apply = silu ? gn_bwd_apply_kernel<T, V, true> : gn_bwd_apply_kernel<T, V, false>;
-    cudaError_t e = allow(sums, smem);
-    if (e == cudaSuccess) e = allow(apply, smem2);
+    cudaError_t e = silu ? allow<gn_bwd_sums_kernel<T, V, true>>(smem)
+                         : allow<gn_bwd_sums_kernel<T, V, false>>(smem);
+    if (e == cudaSuccess)
+        e = silu ? allow<gn_bwd_apply_kernel<T, V, true>>(smem2)
+                 : allow<gn_bwd_apply_kernel<T, V, false>>(smem2);
     steps(d, V);
     const int extra = (d.C + 31) / 32;
     Shape d2 = d;
