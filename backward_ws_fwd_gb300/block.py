@@ -3,6 +3,12 @@ router with its balance loss, and group norm with an activation, channels
 last.  Re-exported by the package; like the rest of it, this module marshals
 tensors into the C calls.  Shapes and types that the C side cannot see are
 checked here (TypeError, ValueError); the rest is checked there (WsfError).
+
+Every operator takes ``stream=`` (the current stream otherwise): results and
+temporary workspaces that it allocates belong to that stream; inputs made on
+another one have to be ready.  Outputs and workspaces may be given by the
+caller; a workspace serves one call at a time (two captured graphs that replay
+at the same time need two).
 """
 from __future__ import annotations
 
