@@ -377,7 +377,8 @@ __device__ __forceinline__ Vals<V> params(const float* p, int ch) {
 // First pass: mean and squared deviations of every group over a tile.  A
 // thread sums about its first value; threads' means and deviations are joined
 // about their common mean, first the row lanes of a channel (Q threads a
-// channel where there are few), then a group's channels by lg lanes.
+// channel where there are few), then a group's channels by lg lanes.  Means are
+// added about one of them, so that a common offset costs no digits.
 template <typename T, int V>
 __global__ void __launch_bounds__(NT, kStatsCtas)
     gn_stats_kernel(const T* x, const Shape d, float* part_m, float* part_q) {
@@ -436,9 +437,11 @@ __global__ void __launch_bounds__(NT, kStatsCtas)
     if (t.RL > 1 && pt.q < pt.Q) {  // into row lane q
         const float n = part_rows[pt.q], inv = n > 0.f ? 1.0f / n : 0.f;
         for (int c = d.C < NT ? (int)threadIdx.x - pt.q * d.C : (int)threadIdx.x; c < d.C; c += NT) {
+            const float ref = sm[pt.q * d.C + c];
             float s = 0.f;
-            for (int r = pt.q; r < t.RL; r += pt.Q) s = fmaf((float)rows.of(r), sm[r * d.C + c], s);
-            const float m = s * inv;
+            for (int r = pt.q; r < t.RL; r += pt.Q)
+                s = fmaf((float)rows.of(r), sm[r * d.C + c] - ref, s);
+            const float m = fmaf(s, inv, ref);
             s = 0.f;
             for (int r = pt.q; r < t.RL; r += pt.Q) {
                 const float e = sm[r * d.C + c] - m;
@@ -454,12 +457,13 @@ __global__ void __launch_bounds__(NT, kStatsCtas)
     for (int g0 = 0; g0 < d.G; g0 += NT / d.lg) {
         const int g = g0 + threadIdx.x / d.lg;
         const bool on = g < d.G;
+        const float ref = on ? sm[g * d.Cg] : 0.f;
         float s = 0.f;
         if (on)
             for (int q = 0; q < pt.Q; q++)
                 for (int c = j0; c < d.Cg; c += d.lg)
-                    s = fmaf(part_rows[q], sm[q * d.C + g * d.Cg + c], s);
-        const float m = lanes_sum(s, d.lg) * inv;
+                    s = fmaf(part_rows[q], sm[q * d.C + g * d.Cg + c] - ref, s);
+        const float m = fmaf(lanes_sum(s, d.lg), inv, ref);
         s = 0.f;
         if (on)
             for (int q = 0; q < pt.Q; q++)
@@ -492,15 +496,17 @@ __global__ void __launch_bounds__(NT) gn_join_kernel(const float* pm, const floa
         pm += u / d.G * d.tiles * d.G + u % d.G;
         pq += u / d.G * d.tiles * d.G + u % d.G;
         const float whole = (float)d.rows, last = (float)(d.S - (d.tiles - 1) * d.rows);
+        const float ref = Sums ? 0.f : __ldcg(pm);
         float s = 0.f, q = 0.f;
 #pragma unroll 8
         for (int i = lane; i < d.tiles; i += 32) {
-            s = fmaf(Sums ? 1.f : i + 1 < d.tiles ? whole : last, __ldcg(pm + (int64_t)i * d.G), s);
+            s = fmaf(Sums ? 1.f : i + 1 < d.tiles ? whole : last,
+                     __ldcg(pm + (int64_t)i * d.G) - ref, s);
             if (Sums) q += __ldcg(pq + (int64_t)i * d.G);
         }
         s = group_sum<32>(s);
         if (!Sums) {
-            s /= (float)d.S;
+            s = ref + s / (float)d.S;
 #pragma unroll 8
             for (int i = lane; i < d.tiles; i += 32) {
                 const float e = __ldcg(pm + (int64_t)i * d.G) - s;
@@ -576,9 +582,10 @@ __global__ void __launch_bounds__(NT, kApplyCtas)
     join(
         d, red,
         [&](int i, int g) {
-            return make_float2((i + 1 < d.joins ? whole : last) * pm[(int64_t)i * d.G + g], 0.f);
+            const float n = i + 1 < d.joins ? whole : last;
+            return make_float2(n * (pm[(int64_t)i * d.G + g] - pm[g]), 0.f);
         },
-        [&](int g, float2 s) { st[g].x = s.x / all; });
+        [&](int g, float2 s) { st[g].x = pm[g] + s.x / all; });
     join(
         d, red,
         [&](int i, int g) {

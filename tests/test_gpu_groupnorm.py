@@ -117,6 +117,14 @@ def test_offsets_outliers_and_constants(wsf, dtype, N, S, C, G):
     _check(wsf, flat.to(dtype), w, b, dy.to(dtype), G, "silu")
 
 
+@pytest.mark.parametrize("N,S,C,G", [(39, 1467, 1, 1), (145, 431, 1, 1), (631, 491, 2, 2), (2, 30000, 3, 1)])
+def test_few_channels_with_an_offset(wsf, N, S, C, G):
+    """Hundreds of threads' means a group, all near 20: they are joined without
+    adding up the offset."""
+    x, w, b, dy = _inputs(N, S, C, torch.float32, 18, mean=0.0)
+    _check(wsf, x + 20.0, w, b, dy, G, "silu")
+
+
 def test_several_chunks(wsf):
     """More values than the passes take at a time: uneven chunks of the batch
     in both directions, gradients summed over them."""
